@@ -363,6 +363,125 @@ TKV_API tkv_status tkv_selftest_wait_timeout(tkv_cache *cache, int64_t limit_cyc
 /* Launch counters since tkv_create (kernels this cache has launched). */
 TKV_API int64_t tkv_launch_count(const tkv_cache *cache);
 
+/* ---------------------------------------------------------------------------
+ * The paged 8-bit cache: position encoding, append and attention for layers and
+ * prompts that are not thought-compressed.  Every token keeps its key and value as
+ * 8-bit codes; a page holds `page` consecutive tokens of every kv head, with one fp32
+ * scale per (page, kv head) for the keys and one for the values:
+ *   k_pool, v_pool    8-bit [pages][Hkv][page][D]
+ *   k_scale, v_scale  fp32  [pages][Hkv]            value = code * scale
+ * Codes are signed integers in [-127, 127] (code 0) or FP8 E4M3 (code 1).  Scales are
+ * finite and >= 0; the append writes powers of two.  Token j of sequence b is in page
+ * block_table[b * max_pages + j / page], slot j % page.  A page that an append writes
+ * belongs to one sequence; pages that are only read may be shared.
+ *
+ * Lengths, offsets and tables are device memory:
+ *   block_table  int32 [B][max_pages]   page of each block of tokens (-1: none)
+ *   kv_len       int32 [B]              tokens of each sequence, the call's own included
+ *   cu           int32 [B + 1] or NULL  rows cu[b] .. cu[b+1] of the call's T rows belong
+ *                                       to sequence b, its last tokens in order; NULL: T = B,
+ *                                       one row for each sequence
+ * Rows before cu[0] and behind cu[B] are not read and their outputs are left as they were.
+ * Row arrays (q, k, v and the outputs) are [rows][heads][D] of the configured type with a
+ * contiguous head dim; token and head strides count elements, are multiples of 4 and the
+ * arrays are 8-byte aligned.  Conditions only the device can see skip what they touch and
+ * latch an error for tkv_paged_poll_error: a page id of -1 or a table that is too short
+ * TKV_ERR_CAPACITY; a page id outside [0, pages), cu that decreases or leaves [0, T] and
+ * lengths below 0 TKV_ERR_INVALID.
+ * ------------------------------------------------------------------------- */
+enum { TKV_CODE_INT8 = 0, TKV_CODE_E4M3 = 1 };
+enum { TKV_DTYPE_BF16 = 0, TKV_DTYPE_FP16 = 1 };
+
+typedef struct {
+    int32_t B;           /* sequences (1 .. 65535)                              */
+    int32_t Hkv;         /* kv heads                                            */
+    int32_t G;           /* query heads per kv head (1 .. 16)                   */
+    int32_t D;           /* head dim: 64 or 128                                 */
+    int32_t page;        /* tokens of a page: 16, 32, 64 or 128                 */
+    int32_t pages;       /* pages of the pools                                  */
+    int32_t max_pages;   /* row length of the block table                       */
+    int32_t code;        /* TKV_CODE_INT8 or TKV_CODE_E4M3                      */
+    int32_t dtype;       /* type of q, k, v and the outputs: TKV_DTYPE_*        */
+} tkv_paged_config;
+
+/* How a row x [D] of a head becomes an encoded one (any part may be absent):
+ *   norm      y = x * w / sqrt(mean(x^2) + eps)      (w = q_weight / k_weight, both or none)
+ *   rotation  for pair i of rot/2, angle th = position * inv_freq[i]:
+ *             (a, b) -> (a cos th - b sin th, a sin th + b cos th)
+ *             a, b = elements i, i + rot/2 (interleaved 0) or 2i, 2i + 1 (interleaved 1);
+ *             elements from rot on stay as they are.
+ * Both in fp32 with one rounding at the end; the angle's turns are reduced in fp64. */
+typedef struct {
+    const float *inv_freq;   /* device fp32 [rot/2], NULL when rot is 0        */
+    int32_t rot;             /* rotated elements: a multiple of 8 in [0, D]    */
+    int32_t interleaved;     /* 0 or 1                                         */
+    const void *q_weight;    /* device [D] of the rows' type, or NULL          */
+    const void *k_weight;
+    float eps;               /* >= 0                                           */
+} tkv_rope;
+
+typedef struct tkv_paged tkv_paged;
+
+/* Norm and rotation of T tokens' queries [T][Hq][D] and keys [T][Hkv][D] in one pass:
+ * position of token t is pos[t] (device int32).  Hq or Hkv may be 0.  Outputs may be the
+ * inputs.  Returns TKV_ERR_INVALID for bad sizes, types, strides or alignment; T = 0 is a
+ * no-op. */
+TKV_API tkv_status tkv_qk_norm_rope(const tkv_rope *rope, const void *q, int64_t q_token_stride,
+                                    int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                                    int64_t k_head_stride, const int32_t *pos, void *q_out, void *k_out,
+                                    int64_t qo_token_stride, int64_t qo_head_stride, int64_t ko_token_stride,
+                                    int64_t ko_head_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                    int32_t dtype, void *stream);
+
+/* Bytes of device workspace a paged cache needs (0 if the configuration is invalid). */
+TKV_API size_t tkv_paged_workspace_bytes(const tkv_paged_config *cfg);
+
+/* Create a paged cache over the caller's pools (16-byte aligned), scales and workspace
+ * (256-byte aligned, at least tkv_paged_workspace_bytes(cfg) bytes).  The device is not
+ * touched: call tkv_paged_reset once before the first use. */
+TKV_API tkv_status tkv_paged_create(const tkv_paged_config *cfg, void *k_pool, void *v_pool, float *k_scale,
+                                    float *v_scale, void *d_workspace, size_t workspace_bytes, tkv_paged **out);
+TKV_API tkv_status tkv_paged_destroy(tkv_paged *cache);
+
+/* Clear the workspace's counters and error word (the pools stay as they are). */
+TKV_API tkv_status tkv_paged_reset(tkv_paged *cache, void *stream);
+
+/* Append the T rows of k and v (cu, kv_len as above; kv_len counts the new tokens), keys
+ * encoded by `rope` (NULL: as they are) at their token's index in its sequence.  With
+ * q != NULL the same launch writes the encoded queries [T][Hkv*G][D] to q_out.  A sequence
+ * with kv_len 0 is padding: its rows are skipped, q_out's too; so are those of a sequence
+ * that an error is latched for (kv_len below its number of rows: TKV_ERR_INVALID).
+ *   max_new   bound on a sequence's new tokens; a sequence with more is skipped
+ *             (TKV_ERR_INVALID latched)
+ * The scale of a page and head becomes the smallest power of two s >= 2^-64 at which every
+ * finite element's magnitude is at most qmax * s (qmax 127 / 448), or stays the larger one
+ * that a page with earlier tokens has; where it grows, the earlier tokens' codes are
+ * rounded again to the new scale.  Codes are the fp32 value / s rounded half to even;
+ * +-infinity becomes the largest code of its sign; NaN becomes E4M3 NaN, or integer 0. */
+TKV_API tkv_status tkv_paged_append(tkv_paged *cache, const tkv_rope *rope, const void *k, int64_t k_token_stride,
+                                    int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                                    int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                                    int64_t q_head_stride, void *q_out, int64_t qo_token_stride,
+                                    int64_t qo_head_stride, int32_t T, const int32_t *block_table,
+                                    const int32_t *kv_len, const int32_t *cu, int32_t max_new, void *stream);
+
+/* GQA attention of T query rows over the cache.  Row i of the n rows of sequence b is at
+ * position p = kv_len[b] - n + i and sees keys max(0, p - window + 1) .. p (window 0: all
+ * keys up to p):  out = sum_j softmax_j(softmax_scale * q . k_j) v_j, rounded once; a row
+ * that sees no key (one at a negative position too) gives zeros, whatever is in q.
+ *   max_q     bound on a sequence's query rows; it only chooses the kernel
+ *   window    >= 0
+ * Tokens of a page that cannot be read (see above) count as masked. */
+TKV_API tkv_status tkv_paged_attention(tkv_paged *cache, const void *q, int64_t q_token_stride,
+                                       int64_t q_head_stride, void *out, int64_t o_token_stride,
+                                       int64_t o_head_stride, int32_t T, const int32_t *block_table,
+                                       const int32_t *kv_len, const int32_t *cu, int32_t max_q, int32_t window,
+                                       float softmax_scale, void *stream);
+
+/* As tkv_poll_error and tkv_launch_count, for a paged cache. */
+TKV_API tkv_status tkv_paged_poll_error(tkv_paged *cache, void *stream);
+TKV_API int64_t tkv_paged_launch_count(const tkv_paged *cache);
+
 /* Human-readable description of the calling thread's last non-OK status. */
 TKV_API const char *tkv_last_error_string(void);
 

@@ -1,0 +1,217 @@
+// paged_api.cu -- host side of the paged 8-bit cache's entry points: configuration and
+// argument checks, the workspace's layout and the launches.
+#include <climits>
+#include <cmath>
+#include <cstdio>
+#include <new>
+#include <string>
+
+#include "paged.cuh"
+
+struct tkv_paged {
+    tkv_paged_config cfg;
+    tkv::paged::View view;
+    int64_t launches;
+};
+
+namespace tkv {
+tkv_status api_fail(tkv_status st, const std::string &msg);
+}
+
+namespace {
+
+using tkv::api_fail;
+using tkv::paged::Rows;
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+const char *config_fault(const tkv_paged_config *c) {
+    if (!c) return "config is NULL";
+    if (c->B < 1 || c->B > 65535) return "B must be in [1, 65535]";
+    if (c->Hkv < 1 || c->G < 1 || c->G > tkv::paged::kMaxGroup) return "Hkv must be >= 1 and G in [1, 16]";
+    if ((long long)c->Hkv * c->G > 65535) return "Hkv * G must be <= 65535";
+    if ((long long)c->B * c->Hkv > (1 << 24)) return "B * Hkv must be <= 2^24";
+    if (c->D != 64 && c->D != 128) return "D must be 64 or 128";
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return "page must be 16, 32, 64 or 128";
+    if (c->pages < 1 || c->max_pages < 1) return "pages and max_pages must be >= 1";
+    if ((long long)c->max_pages * c->page > (1ll << 30)) return "max_pages * page must be <= 2^30";
+    if ((long long)c->pages * c->Hkv > INT_MAX) return "pages * Hkv must be < 2^31";
+    if (c->code != TKV_CODE_INT8 && c->code != TKV_CODE_E4M3) return "code must be TKV_CODE_INT8 or TKV_CODE_E4M3";
+    if (c->dtype != TKV_DTYPE_BF16 && c->dtype != TKV_DTYPE_FP16) return "dtype must be TKV_DTYPE_BF16 or TKV_DTYPE_FP16";
+    return nullptr;
+}
+
+const char *rope_fault(const tkv_rope *r, int D) {
+    if (r->rot < 0 || r->rot > D || r->rot % 8) return "rot must be a multiple of 8 in [0, D]";
+    if (r->rot > 0 && (!r->inv_freq || !aligned(r->inv_freq, 4))) return "inv_freq is NULL or not 4-byte aligned";
+    if (r->interleaved != 0 && r->interleaved != 1) return "interleaved must be 0 or 1";
+    if ((r->q_weight == nullptr) != (r->k_weight == nullptr)) return "q_weight and k_weight: both or none";
+    if (!aligned(r->q_weight, 2) || !aligned(r->k_weight, 2)) return "weights must be 2-byte aligned";
+    if (r->q_weight && !(r->eps >= 0.f && std::isfinite(r->eps))) return "eps must be finite and >= 0";
+    return nullptr;
+}
+
+// Rows of one call: pointers and strides that eight-byte accesses can use.
+const char *rows_fault(const Rows &r) {
+    if (!r.p) return "NULL row array";
+    if (!aligned(r.p, 8)) return "row arrays must be 8-byte aligned";
+    if (r.token % 4 || r.head % 4) return "row strides must be multiples of 4 elements";
+    if (r.token < 0 || r.head < 0) return "row strides must be >= 0";
+    return nullptr;
+}
+const char *out_fault(const Rows &r, int T, int heads, int D) {
+    if (const char *w = rows_fault(r)) return w;
+    // rows that overlap would be written by several threads
+    if ((heads > 1 && r.head < D) || (T > 1 && r.token < D)) return "output rows overlap";
+    return nullptr;
+}
+
+tkv_status cuda_status(cudaError_t e, const char *what) {
+    if (e == cudaSuccess) return TKV_OK;
+    return api_fail(TKV_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+tkv_status bad(const char *why) { return api_fail(TKV_ERR_INVALID, why); }
+
+const char *lengths_fault(const tkv_paged *c, const int32_t *table, const int32_t *len, const int32_t *cu, int T) {
+    if (!table || !len) return "NULL block_table or kv_len";
+    if (!aligned(table, 4) || !aligned(len, 4) || !aligned(cu, 4)) return "int32 arrays must be 4-byte aligned";
+    if (T < 0) return "T must be >= 0";
+    if (!cu && T != c->cfg.B) return "without cu, T must be B";
+    return nullptr;
+}
+
+}  // namespace
+
+namespace tkv {
+namespace paged {
+size_t attention_workspace_bytes(const tkv_paged_config &cfg);
+}
+}  // namespace tkv
+
+extern "C" {
+
+tkv_status tkv_qk_norm_rope(const tkv_rope *rope, const void *q, int64_t qt, int64_t qh, const void *k, int64_t kt,
+                            int64_t kh, const int32_t *pos, void *q_out, void *k_out, int64_t qot, int64_t qoh,
+                            int64_t kot, int64_t koh, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                            void *stream) {
+    if (!rope) return bad("rope is NULL");
+    if (D != 64 && D != 128) return bad("D must be 64 or 128");
+    if (dtype != TKV_DTYPE_BF16 && dtype != TKV_DTYPE_FP16) return bad("dtype must be TKV_DTYPE_BF16 or TKV_DTYPE_FP16");
+    if (T < 0 || Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535) return bad("T, Hq or Hkv out of range");
+    if (const char *w = rope_fault(rope, D)) return bad(w);
+    if (T == 0 || Hq + Hkv == 0) return TKV_OK;
+    if (!pos || !aligned(pos, 4)) return bad("pos is NULL or not 4-byte aligned");
+    Rows qr{q, qt, qh}, kr{k, kt, kh}, qor{q_out, qot, qoh}, kor{k_out, kot, koh};
+    if (Hq > 0) {
+        if (const char *w = rows_fault(qr)) return bad(w);
+        if (const char *w = out_fault(qor, T, Hq, D)) return bad(w);
+    }
+    if (Hkv > 0) {
+        if (const char *w = rows_fault(kr)) return bad(w);
+        if (const char *w = out_fault(kor, T, Hkv, D)) return bad(w);
+    }
+    return cuda_status(tkv::paged::launch_norm_rope(*rope, qr, kr, pos, qor, kor, T, Hq, Hkv, D, dtype,
+                                                    static_cast<cudaStream_t>(stream)),
+                       "tkv_qk_norm_rope");
+}
+
+size_t tkv_paged_workspace_bytes(const tkv_paged_config *cfg) {
+    if (const char *w = config_fault(cfg)) { api_fail(TKV_ERR_INVALID, w); return 0; }
+    return 256 + tkv::paged::attention_workspace_bytes(*cfg);
+}
+
+tkv_status tkv_paged_create(const tkv_paged_config *cfg, void *k_pool, void *v_pool, float *k_scale, float *v_scale,
+                            void *d_workspace, size_t workspace_bytes, tkv_paged **out) {
+    if (!out) return bad("out is NULL");
+    *out = nullptr;
+    if (const char *w = config_fault(cfg)) return bad(w);
+    if (!k_pool || !v_pool || !k_scale || !v_scale) return bad("NULL pool or scale pointer");
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return bad("pools must be 16-byte aligned");
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return bad("scales must be 4-byte aligned");
+    if (!d_workspace || !aligned(d_workspace, 256)) return bad("workspace must be 256-byte aligned and not NULL");
+    if (workspace_bytes < tkv_paged_workspace_bytes(cfg)) return bad("workspace too small");
+    auto *c = new (std::nothrow) tkv_paged();
+    if (!c) return bad("out of host memory");
+    c->cfg = *cfg;
+    c->launches = 0;
+    int lg = 0;
+    while ((1 << lg) < cfg->page) ++lg;
+    c->view = {cfg->B, cfg->Hkv, cfg->G, cfg->D, cfg->page, lg, cfg->pages, cfg->max_pages, cfg->code, cfg->dtype,
+               static_cast<uint8_t *>(k_pool), static_cast<uint8_t *>(v_pool), k_scale, v_scale,
+               static_cast<uint32_t *>(d_workspace)};
+    *out = c;
+    return TKV_OK;
+}
+
+tkv_status tkv_paged_destroy(tkv_paged *c) {
+    delete c;
+    return TKV_OK;
+}
+
+tkv_status tkv_paged_reset(tkv_paged *c, void *stream) {
+    if (!c) return bad("cache is NULL");
+    return cuda_status(cudaMemsetAsync(c->view.err, 0, 256, static_cast<cudaStream_t>(stream)), "tkv_paged_reset");
+}
+
+tkv_status tkv_paged_append(tkv_paged *c, const tkv_rope *rope, const void *k, int64_t kt, int64_t kh, const void *v,
+                            int64_t vt, int64_t vh, const void *q, int64_t qt, int64_t qh, void *q_out, int64_t qot,
+                            int64_t qoh, int32_t T, const int32_t *block_table, const int32_t *kv_len,
+                            const int32_t *cu, int32_t max_new, void *stream) {
+    if (!c) return bad("cache is NULL");
+    if (const char *w = lengths_fault(c, block_table, kv_len, cu, T)) return bad(w);
+    const tkv_rope none{};
+    const tkv_rope &r = rope ? *rope : none;
+    if (const char *w = rope_fault(&r, c->cfg.D)) return bad(w);
+    if (max_new < 1 || max_new > (1 << 30)) return bad("max_new must be in [1, 2^30]");
+    if (T == 0) return TKV_OK;
+    Rows kr{k, kt, kh}, vr{v, vt, vh}, qr{q, qt, qh}, qor{q_out, qot, qoh};
+    if (const char *w = rows_fault(kr)) return bad(w);
+    if (const char *w = rows_fault(vr)) return bad(w);
+    if (q) {
+        if (const char *w = rows_fault(qr)) return bad(w);
+        if (const char *w = out_fault(qor, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
+    } else if (q_out) {
+        return bad("q_out without q");
+    }
+    return cuda_status(tkv::paged::launch_append(c->view, r, kr, vr, qr, qor, T, block_table, kv_len, cu,
+                                                 max_new < T ? max_new : T, static_cast<cudaStream_t>(stream),
+                                                 &c->launches),
+                       "tkv_paged_append");
+}
+
+tkv_status tkv_paged_attention(tkv_paged *c, const void *q, int64_t qt, int64_t qh, void *out, int64_t ot, int64_t oh,
+                               int32_t T, const int32_t *block_table, const int32_t *kv_len, const int32_t *cu,
+                               int32_t max_q, int32_t window, float softmax_scale, void *stream) {
+    if (!c) return bad("cache is NULL");
+    if (const char *w = lengths_fault(c, block_table, kv_len, cu, T)) return bad(w);
+    if (max_q < 1) return bad("max_q must be >= 1");
+    if (window < 0) return bad("window must be >= 0");
+    if (!std::isfinite(softmax_scale)) return bad("softmax_scale must be finite");
+    if (T == 0) return TKV_OK;
+    Rows qr{q, qt, qh}, outr{out, ot, oh};
+    if (const char *w = rows_fault(qr)) return bad(w);
+    if (const char *w = out_fault(outr, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
+    return cuda_status(tkv::paged::launch_attention(c->view, qr, outr, T, block_table, kv_len, cu, max_q, window,
+                                                    softmax_scale, static_cast<cudaStream_t>(stream), &c->launches),
+                       "tkv_paged_attention");
+}
+
+tkv_status tkv_paged_poll_error(tkv_paged *c, void *stream) {
+    if (!c) return bad("cache is NULL");
+    auto st = static_cast<cudaStream_t>(stream);
+    uint32_t w[4] = {0, 0, 0, 0};
+    cudaError_t e = cudaMemcpyAsync(w, c->view.err, sizeof(w), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(c->view.err, 0, sizeof(w), st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_status(e, "tkv_paged_poll_error");
+    if (w[0] == 0) return TKV_OK;
+    char msg[160];
+    std::snprintf(msg, sizeof(msg), "device error %u (%u occurrences, detail %u)", w[0], w[1], w[2]);
+    return api_fail(static_cast<tkv_status>(w[0]), msg);
+}
+
+int64_t tkv_paged_launch_count(const tkv_paged *c) { return c ? c->launches : 0; }
+
+}  // extern "C"

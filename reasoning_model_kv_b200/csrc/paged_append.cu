@@ -1,0 +1,265 @@
+// paged_append.cu -- new keys (encoded on the way) and values into the paged 8-bit cache.
+//
+// A unit is one (page, kv head) of the keys or of the values: its threads hold the page's
+// new rows in registers (four passes of rows, eight elements a lane), find their largest
+// magnitude, settle the scale, round what the page held before if the scale grew, and write
+// the codes.  So the rows are read once, a scale has one writer and nothing needs an atomic.
+// Units of small pages share a block.  The queries' rows are blocks of the same launch.
+#include <climits>
+
+#include <cuda_fp8.h>
+
+#include "encode_rows.cuh"
+
+namespace tkv {
+namespace paged {
+namespace {
+
+constexpr int kPasses = 4;
+
+__device__ __forceinline__ void unit_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// The smallest power of two s >= 2^-64 with qmax * s >= amax (amax finite).
+template <int CODE>
+__device__ __forceinline__ float pow2_scale(float amax) {
+    // amax = f * 2^e with f in [1/2, 1); qmax = fq * 2^eq; 2^(e - eq), once more if f > fq
+    constexpr int eq = CODE == TKV_CODE_E4M3 ? 9 : 7;
+    constexpr uint32_t fq = CODE == TKV_CODE_E4M3 ? 0x600000u : 0x7E0000u;   // 448 = 1.75 * 2^8, 127 = 1.984375 * 2^6
+    const uint32_t u = __float_as_uint(amax);
+    int x = (int)(u >> 23) - 126 - eq + ((u & 0x7fffffu) > fq ? 1 : 0);
+    x = max(x, -64);
+    return __uint_as_float((uint32_t)(x + 127) << 23);
+}
+
+// Four codes of x, which are values over the scale.
+template <int CODE>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    if constexpr (CODE == TKV_CODE_E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    } else {
+        // (int)NaN is 0, and values beyond 127 only come from infinities
+        auto q = [](float x) { return (uint32_t)(int)fminf(fmaxf(x == x ? rintf(x) : 0.f, -127.f), 127.f) & 0xffu; };
+        return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+    }
+}
+template <int CODE>
+__device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
+    if constexpr (CODE == TKV_CODE_E4M3) {
+        const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
+        const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
+        const float2 a = __half22float2(lo), b = __half22float2(hi);
+        x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
+    }
+}
+
+struct AppendArgs {
+    View c;
+    tkv_rope rope;
+    Rows k, v, q, qo;
+    const int32_t *block_table, *kv_len, *cu;
+    int T, max_new, slots;         // slots: pages that a sequence's new tokens can touch
+    long long units, kv_blocks;
+    int q_groups, q_per;
+};
+
+// Threads of a unit (UT = page * D / 32) and of a block.
+__host__ __device__ constexpr int block_threads(int ut) { return ut > 256 ? ut : 256; }
+
+template <typename T, int D, int CODE, int UT>
+__global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendArgs a) {
+    constexpr int kBlock = block_threads(UT);
+    const View &c = a.c;
+    if ((long long)blockIdx.x >= a.kv_blocks) {      // the queries
+        const long long w = ((long long)blockIdx.x - a.kv_blocks) * (kBlock / 32) + (threadIdx.x >> 5);
+        const int t = (int)(w / a.q_groups), lane = threadIdx.x & 31;
+        if (t >= a.T) return;
+        int b = t;
+        if (a.cu) {     // the sequence of row t: as many ends as are not behind it
+            b = 0;
+            for (int i = 0; i < c.B; i += 32) b += __popc(__ballot_sync(0xffffffffu, i + lane < c.B && a.cu[i + lane + 1] <= t));
+        }
+        Seq s;
+        uint32_t bad;
+        // what is wrong with a sequence is reported by its keys' units
+        if (b >= c.B || !load_seq(a.cu, a.kv_len, b, a.T, &s, &bad) || t < s.row0 || t >= s.row0 + s.n ||
+            s.n > a.max_new || s.len < s.n)
+            return;
+        const int h0 = (int)(w - (long long)t * a.q_groups) * a.q_per;
+        encode_rows<T, D>(a.rope, a.q, Rows{}, a.qo, Rows{}, t, s.len - s.n + (t - s.row0), h0,
+                          min(h0 + a.q_per, c.Hkv * c.G), c.Hkv * c.G);
+        return;
+    }
+    __shared__ float red[kBlock / 32];
+    const int unit_in_block = threadIdx.x / UT, tid = threadIdx.x % UT;
+    const long long unit = (long long)blockIdx.x * (kBlock / UT) + unit_in_block;
+    if (unit >= a.units) return;
+    const int h = (int)(unit % c.Hkv);
+    long long rest = unit / c.Hkv;
+    const bool values = rest & 1;
+    rest >>= 1;
+    const int slot = (int)(rest % a.slots), b = (int)(rest / a.slots);
+    Seq s;
+    uint32_t bad = 0;
+    bool ok = load_seq(a.cu, a.kv_len, b, a.T, &s, &bad);
+    if (ok && s.len == 0) return;                             // padding
+    if (ok && s.n > a.max_new) { ok = false; bad = kBadRows; }
+    if (ok && s.len < s.n) { ok = false; bad = kBadLen; }
+    if (!ok) {
+        if (tid == 0 && slot == 0 && h == 0 && !values) latch(c, bad);
+        return;
+    }
+    const int start = s.len - s.n, p = (start >> c.page_log2) + slot;
+    const long long first = (long long)p << c.page_log2;      // the page's first token
+    if (s.n == 0 || first >= s.len) return;
+    const int id = load_page(c, a.block_table, b, p, &bad);
+    if (id < 0) {
+        if (tid == 0 && h == 0 && !values) latch(c, bad);
+        return;
+    }
+    constexpr int L = D / 8, kRows = UT / L;                  // rows of a pass
+    const int j = tid & (L - 1), r0 = tid / L;
+    const int lo = max(0, (int)(start - first)), hi = min(c.page, (int)(s.len - first));
+    const Rows &x_in = values ? a.v : a.k;
+    const Chunks ch = row_chunks(a.rope, j);
+    uint2 in0[kPasses], in1[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * kRows + r0;
+        in0[i] = in1[i] = make_uint2(0, 0);
+        if (r >= lo && r < hi) {
+            const T *src = static_cast<const T *>(x_in.p) + (s.row0 + (first + r - start)) * x_in.token + h * x_in.head;
+            in0[i] = *reinterpret_cast<const uint2 *>(src + ch.a);
+            in1[i] = *reinterpret_cast<const uint2 *>(src + ch.b);
+        }
+    }
+    const size_t ps = (size_t)id * c.Hkv + h;
+    float *const scale = (values ? c.v_scale : c.k_scale) + ps;
+    const float old = lo > 0 ? *scale : 0.f;
+    float x[kPasses][8];
+    float w[8];
+    double f[4];
+    const bool norm = !values && a.rope.k_weight != nullptr, turn = !values && ch.turns;
+    if (norm) load_weights<T>(a.rope.k_weight, ch, w);
+    load_turns(a.rope, j, turn, f);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * kRows + r0;
+        unpack8<T>(in0[i], in1[i], x[i]);
+        if (i * kRows < hi && (i + 1) * kRows > lo) {        // the same for all the unit's threads
+            if (norm) row_norm<D>(x[i], w, a.rope.eps);
+            if (turn) {
+                float cs[4], sn[4];
+                turn_angles(f, (int)(first + r), cs, sn);
+                row_turn(x[i], cs, sn, a.rope.interleaved);
+            }
+        }
+        if (r >= lo && r < hi) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float m = fabsf(x[i][e]);
+                if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);      // finite ones
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (UT > 32) {
+        if ((tid & 31) == 0) red[threadIdx.x >> 5] = amax;
+        unit_sync(1 + unit_in_block, UT);
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < UT / 32; ++i) amax = fmaxf(amax, red[unit_in_block * (UT / 32) + i]);
+    }
+    const float now = fmaxf(pow2_scale<CODE>(amax), old);     // the same in all the unit's threads
+    uint8_t *const pool = (values ? c.v_pool : c.k_pool) + ((ps << c.page_log2) * D);
+    const float inv = 1.f / now;
+    const bool exact = (__float_as_uint(now) & 0x7fffffu) == 0;    // a power of two: 1 / now is exact
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int r = i * kRows + r0;
+        if (r >= hi) continue;
+        uint32_t *const c0 = reinterpret_cast<uint32_t *>(pool + r * D + ch.a);
+        uint32_t *const c1 = reinterpret_cast<uint32_t *>(pool + r * D + ch.b);
+        if (r < lo) {
+            if (now == old) continue;
+            const float ratio = old / now;
+            float y[4], z[4];
+            values4<CODE>(*c0, y);
+            values4<CODE>(*c1, z);
+            *c0 = codes4<CODE>(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+            *c1 = codes4<CODE>(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio);
+        } else {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = exact ? x[i][e] * inv : x[i][e] / now;
+            *c0 = codes4<CODE>(y[0], y[1], y[2], y[3]);
+            *c1 = codes4<CODE>(y[4], y[5], y[6], y[7]);
+        }
+    }
+    // every thread of the unit has read the old scale before the barrier above (or is of the
+    // one warp that read it together)
+    if constexpr (UT == 32) __syncwarp();
+    if (tid == 0) *scale = now;
+}
+
+template <typename T, int D, int CODE, int UT>
+cudaError_t run(AppendArgs a, cudaStream_t st) {
+    constexpr int kBlock = block_threads(UT);
+    const long long per = kBlock / UT;
+    a.units = 2ll * a.c.B * a.slots * a.c.Hkv;
+    a.kv_blocks = (a.units + per - 1) / per;
+    long long q_blocks = 0;
+    if (a.q.p != nullptr) {
+        const int heads = a.c.Hkv * a.c.G;
+        a.q_per = heads_per_warp<D>(a.T, heads);
+        a.q_groups = (heads + a.q_per - 1) / a.q_per;
+        q_blocks = ((long long)a.T * a.q_groups + kBlock / 32 - 1) / (kBlock / 32);
+    }
+    if (a.kv_blocks + q_blocks > INT_MAX) return cudaErrorInvalidValue;
+    append_kernel<T, D, CODE, UT><<<(unsigned)(a.kv_blocks + q_blocks), kBlock, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, int D, int CODE>
+cudaError_t run_page(const AppendArgs &a, cudaStream_t st) {
+    switch (a.c.page) {
+        case 16: return run<T, D, CODE, 16 * D / 32>(a, st);
+        case 32: return run<T, D, CODE, 32 * D / 32>(a, st);
+        case 64: return run<T, D, CODE, 64 * D / 32>(a, st);
+        default: return run<T, D, CODE, 128 * D / 32>(a, st);
+    }
+}
+template <typename T>
+cudaError_t run_type(const AppendArgs &a, cudaStream_t st) {
+    if (a.c.code == TKV_CODE_E4M3)
+        return a.c.D == 64 ? run_page<T, 64, TKV_CODE_E4M3>(a, st) : run_page<T, 128, TKV_CODE_E4M3>(a, st);
+    return a.c.D == 64 ? run_page<T, 64, TKV_CODE_INT8>(a, st) : run_page<T, 128, TKV_CODE_INT8>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const View &c, const tkv_rope &rope, Rows k, Rows v, Rows q, Rows qo, int T,
+                          const int32_t *block_table, const int32_t *kv_len, const int32_t *cu, int max_new,
+                          cudaStream_t st, int64_t *launches) {
+    AppendArgs a{};
+    a.c = c;
+    a.rope = rope;
+    a.k = k; a.v = v; a.q = q; a.qo = qo;
+    a.block_table = block_table; a.kv_len = kv_len; a.cu = cu;
+    a.T = T; a.max_new = max_new;
+    // max_new tokens that begin at a page's last slot
+    a.slots = (int)(((long long)max_new + 2 * c.page - 2) >> c.page_log2);
+    const cudaError_t e = c.dtype == TKV_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, st) : run_type<__half>(a, st);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace paged
+}  // namespace tkv
