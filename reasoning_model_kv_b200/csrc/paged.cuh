@@ -13,6 +13,7 @@ namespace tkv {
 namespace paged {
 
 constexpr int kMaxGroup = 16;          // query heads per kv head
+constexpr int kMaxLen = 1 << 30;       // tokens of a sequence
 
 struct View {
     int B, Hkv, G, D, page, page_log2, pages, max_pages, code, dtype;
@@ -30,7 +31,7 @@ struct Rows {
 // Detail words of latched errors.
 enum : uint32_t {
     kBadRows = 0x501,     // cu decreases or leaves [0, T], or more rows than max_new
-    kBadLen = 0x502,      // kv_len below 0 or below the sequence's rows
+    kBadLen = 0x502,      // kv_len below 0, above kMaxLen, or (append) below the sequence's rows
     kBadPage = 0x503,     // page id outside [0, pages)
     kNoPage = 0x504,      // page id -1, or the table's row is too short
 };
@@ -49,7 +50,7 @@ __device__ __forceinline__ bool load_seq(const int32_t *cu, const int32_t *kv_le
     s->n = r1 - r0;
     s->len = kv_len[b];
     if (r0 < 0 || r1 < r0 || r1 > T) { *bad = kBadRows; return false; }
-    if (s->len < 0) { *bad = kBadLen; return false; }
+    if (s->len < 0 || s->len > kMaxLen) { *bad = kBadLen; return false; }
     return true;
 }
 

@@ -86,6 +86,7 @@ const char *lengths_fault(const tkv_paged *c, const int32_t *table, const int32_
 namespace tkv {
 namespace paged {
 size_t attention_workspace_bytes(const tkv_paged_config &cfg);
+size_t attention_reset_bytes();      // at the workspace's start, behind the error word
 }
 }  // namespace tkv
 
@@ -151,7 +152,7 @@ tkv_status tkv_paged_destroy(tkv_paged *c) {
 
 tkv_status tkv_paged_reset(tkv_paged *c, void *stream) {
     if (!c) return bad("cache is NULL");
-    return cuda_status(cudaMemsetAsync(c->view.err, 0, 256, static_cast<cudaStream_t>(stream)), "tkv_paged_reset");
+    return cuda_status(cudaMemsetAsync(c->view.err, 0, 256 + tkv::paged::attention_reset_bytes(), static_cast<cudaStream_t>(stream)), "tkv_paged_reset");
 }
 
 tkv_status tkv_paged_append(tkv_paged *c, const tkv_rope *rope, const void *k, int64_t kt, int64_t kh, const void *v,
