@@ -22,7 +22,8 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libtkv.so"
 LIB_DEBUG = PKG / "libtkv_debug.so"
 SOURCES = ["tkv_api.cu", "append.cu", "attention.cu", "attention_i8.cu", "attention_ws.cu", "evict.cu", "noalloc.cu",
-           "selftest.cu", "evict_segments.cu", "norm_rope.cu", "paged_append.cu", "paged_attention.cu", "paged_attention_rows.cu", "paged_api.cu"]
+           "selftest.cu", "evict_segments.cu", "norm_rope.cu", "paged_append.cu", "paged_attention.cu", "paged_attention_rows.cu",
+           "paged_attention_tiles.cu", "paged_join.cu", "paged_api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

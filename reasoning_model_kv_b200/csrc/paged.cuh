@@ -34,6 +34,7 @@ enum : uint32_t {
     kBadLen = 0x502,      // kv_len below 0, above kMaxLen, or (append) below the sequence's rows
     kBadPage = 0x503,     // page id outside [0, pages)
     kNoPage = 0x504,      // page id -1, or the table's row is too short
+    kWaitTimeout = 0x505, // a bounded wait inside a kernel gave up
 };
 
 // The rows and length of sequence b: first row, number of rows, tokens in the cache (fewer

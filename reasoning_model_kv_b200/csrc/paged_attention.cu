@@ -9,7 +9,7 @@ namespace tkv {
 namespace paged {
 
 size_t attention_workspace_bytes(const tkv_paged_config &cfg) {
-    return kArrivedBytes + rows_workspace_bytes(cfg.D);
+    return kArrivedBytes + kCutBytes + std::max(rows_workspace_bytes(cfg.D), tiles_workspace_bytes(cfg.D));
 }
 
 size_t attention_reset_bytes() { return kArrivedBytes; }
@@ -23,8 +23,10 @@ cudaError_t launch_attention(const View &c, Rows q, Rows out, int T, const int32
     a.T = T; a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.arrived = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(c.err) + 256);
-    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.arrived) + kArrivedBytes);
+    a.cut = reinterpret_cast<CutItem *>(reinterpret_cast<uint8_t *>(a.arrived) + kArrivedBytes);
+    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.cut) + kCutBytes);
     const long long rows = (long long)c.G * std::min(cu ? max_q : 1, T);
+    if (rows > 32) return launch_tiles(a, st, launches);
     const cudaError_t e = launch_rows(a, rows, st);
     if (e == cudaSuccess) ++*launches;
     return e;

@@ -12,12 +12,11 @@
 // to the largest scale so far (P in fp16 times 2^7: weights down to 2^-31 of the largest
 // count; they are rounded to 11 bits, more than either output type keeps).
 // The maximum moves only when a logit passes it by 2^8, so most tiles rescale nothing.
-#include <cuda_fp8.h>
-
 #include <type_traits>
 
 #include "norm_rope.cuh"
 #include "paged_attention.cuh"
+#include "paged_codes.cuh"
 
 namespace tkv {
 namespace paged {
@@ -58,29 +57,6 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
     else return (r >> 1) * 128 + (((((r & 1) << 2) + c) ^ (r & 6)) << 4);
 }
-
-// Codes 0, 1 (lo) and 2, 3 (hi) of a word as fp16 pairs.
-template <int CODE>
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (CODE == TKV_CODE_E4M3) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
-        hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 bias = attn::u32_as_h2(0x64806480u);       // 1024 + 128
-        lo = attn::h2_as_u32(__hsub2(attn::u32_as_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
-        hi = attn::h2_as_u32(__hsub2(attn::u32_as_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ T to_out(float x);
-template <>
-__device__ __forceinline__ __half to_out<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 struct Stage {
     float ks, vs;      // the page's scales

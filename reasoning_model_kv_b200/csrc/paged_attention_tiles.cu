@@ -1,0 +1,526 @@
+// paged_attention_tiles.cu -- attention of many query rows (prompt chunks, long verification
+// steps) over the paged 8-bit cache, on the 5th-generation tensor cores.
+//
+// One resident block per SM; an item is up to two tiles of 128 query rows (tokens x the G
+// heads of a kv head) against units of 128 keys.  Warpgroups 0 and 1 hold a row a thread and
+// do the softmax, warpgroup 2 turns the cache's codes into fp16 operands (exact for both code
+// types) in shared memory, one thread of warpgroup 3 issues the matrix instructions:
+//   S [128 x 128] = Q K^T   (Q, K in shared memory, K-major, 128-byte swizzle)
+//   O [128 x D]  += P V     (P fp16 in tensor memory over S, V in shared memory, MN-major)
+// With two tiles of rows the tensor cores work on one while the other is in its softmax, and
+// converting a key costs 1/256 of a row's work.
+// A page's two scales enter as y = x + log2(value scale) in place of the logit x: P = 2^(y - M)
+// carries the value scale, O = sum P code, and the softmax sum is sum P / value scale, so both
+// have one running maximum M, which moves only when y passes it by 2^8.  P is fp16 times 2^7
+// (11 bits, more than either output type keeps; down to 2^-31 of the largest).
+#include <cuda_fp8.h>
+
+#include "norm_rope.cuh"
+#include "paged_attention.cuh"
+#include "paged_codes.cuh"
+#include "tcgen05.cuh"
+
+namespace tkv {
+namespace paged {
+namespace {
+
+using attn::ex2;
+using attn::kFull;
+using attn::mbar_arrive;
+using attn::mbar_wait;
+using attn::smem_addr;
+
+constexpr int kThreads = 512, kUnitLog2 = 7, kUnit = 128;
+constexpr int kChunks = kUnit / 16;      // groups of keys that share a page
+constexpr int kConstSets = 4;
+constexpr float kTiny = 1e-37f;          // factors of logits stay above zero: -inf times one is -inf
+constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of tile s at 128 s, O at 256 + 128 s
+
+template <int D>
+struct Layout {
+    static constexpr int kTile = 128 * D * 2;                  // a tile of fp16 operands
+    static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBytes = 6 * kTile + 1024;
+};
+
+// What the softmax needs of 16 keys: key scale times the softmax scale (log2 units), log2 of
+// the value scale, its inverse.
+struct __align__(16) ChunkConst {
+    float f, lb, iv, pad;
+};
+
+struct Barriers {
+    uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
+    uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t c_full[kConstSets], drain;
+};
+
+// Byte offset of the 16-byte chunk (8 dims) ch of row r in a [128][D] fp16 tile: atoms of 64
+// dims, 128-byte swizzle.
+__device__ __forceinline__ uint32_t operand_at(int r, int ch) {
+    return (ch >> 3) * 16384 + r * 128 + (((ch ^ r) & 7) << 4);
+}
+
+// A bounded wait with one answer for the whole warp.
+__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) {
+    return __all_sync(kFull, mbar_wait(smem_addr(bar), parity));
+}
+
+__device__ __forceinline__ void st128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <typename T, int D, int CODE>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ AttnArgs a) {
+    using L = Layout<D>;
+    constexpr int kPartFloats = 256 * (D + 2);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Plan plan;
+    __shared__ __align__(8) Barriers bar;
+    __shared__ ChunkConst consts[kConstSets][kChunks];
+    __shared__ uint32_t tmem_base;
+    const View &c = a.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int sub_tokens = 128 / c.G;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar.k_full[i], 4);
+            tc::mbar_init(&bar.v_full[i], 4);
+            tc::mbar_init(&bar.k_free[i], 1);
+            tc::mbar_init(&bar.v_free[i], 1);
+            tc::mbar_init(&bar.q_ready[i], 4);
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.p_ready[i], 4);
+            tc::mbar_init(&bar.o_full[i], 1);
+        }
+        for (int i = 0; i < kConstSets; ++i) tc::mbar_init(&bar.c_full[i], 4);
+        tc::mbar_init(&bar.drain, 1);
+        tc::mbar_init_fence();
+    }
+    if (warp == 12) tc::alloc(smem_addr(&tmem_base), 512);
+    long long begin, share;
+    make_plan<kThreads>(a, plan, kUnitLog2, &begin, &share);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tb = tmem_base;
+    const long long end = min(begin + share, plan.total);
+    bool ok = true;
+    if (begin >= plan.total) {
+        if (tid == 0 && a.cut) a.cut[blockIdx.x].parts = 0;
+    } else {
+        Cursor k;
+        cursor_start(a, plan, begin, kUnitLog2, &k);
+        long long at = begin;
+        uint32_t n_tile = 0, n_item = 0;          // units and items behind
+        uint32_t n_tile1 = 0, n_item1 = 0;        // of the second tile of rows
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+            const int sub = warp >> 2, row = tid & 127;
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+            const uint32_t s_col = tb + lanes + kColS + 128 * sub, o_col = tb + lanes + kColO + 128 * sub;
+            const int ti = row / c.G, hd = row - ti * c.G;
+            if (tid == 0 && a.cut) a.cut[blockIdx.x].parts = 0;
+            for (;;) {
+                const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
+                const int tokens = min(a.tile_tokens, k.s.n - k.i0);
+                if (sub == 0 || tokens > sub_tokens) {
+                    const int tok = sub * sub_tokens + ti;
+                    const bool live = ti < sub_tokens && tok < tokens;
+                    // ---- the row's query into the operand tile
+                    float qinv = 1.f;
+                    {
+                        const T *src = static_cast<const T *>(a.q.p) + (long long)(k.s.row0 + k.i0 + tok) * a.q.token +
+                                       (long long)(k.h * c.G + hd) * a.q.head;
+                        const uint32_t dst = sm + L::kQ + sub * L::kTile;
+                        uint2 raw[D / 4];
+#pragma unroll
+                        for (int i = 0; i < D / 4; ++i)
+                            raw[i] = live ? *reinterpret_cast<const uint2 *>(src + 4 * i) : make_uint2(0, 0);
+                        float f = 1.f;
+                        if constexpr (!std::is_same<T, __half>::value) {
+                            // a power of two brings the row's largest element to 2^8
+                            float mx = 0.f;
+#pragma unroll
+                            for (int i = 0; i < D / 4; ++i) {
+                                const float2 u = unpack2<T>(raw[i].x), v = unpack2<T>(raw[i].y);
+                                mx = fmaxf(fmaxf(mx, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+                            }
+                            const int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                            const int sh = e >= 128 ? 0 : min(8 - e, 126);
+                            f = __uint_as_float((uint32_t)(sh + 127) << 23);
+                            qinv = __uint_as_float((uint32_t)(127 - sh) << 23);
+                        }
+                        if (a.scale_log2 < 0.f) f = -f;       // the keys' factors are not negative
+#pragma unroll
+                        for (int i = 0; i < D / 4; i += 2) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float2 u = unpack2<T>(raw[i + j].x), v = unpack2<T>(raw[i + j].y);
+                                w[2 * j] = attn::f32x2_to_f16x2(u.x * f, u.y * f);
+                                w[2 * j + 1] = attn::f32x2_to_f16x2(v.x * f, v.y * f);
+                            }
+                            st128(dst + operand_at(row, i / 2), w[0], w[1], w[2], w[3]);
+                        }
+                        attn::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&bar.q_ready[sub]));
+                    }
+                    const int pos = k.r.first + tok;
+                    const int sub_first = k.r.first + sub * sub_tokens, sub_last = sub_first + sub_tokens - 1;
+                    float M = attn::kNoMax, z = 0.f;
+                    const uint32_t base = sub ? n_tile1 : n_tile;       // tiles of this half before the item
+                    for (int i = 0; i < nu && ok; ++i) {
+                        const uint32_t n = base + i, kt = n_tile + i;
+                        ok = warp_wait(&bar.c_full[kt & (kConstSets - 1)], (kt / kConstSets) & 1) &&
+                             warp_wait(&bar.s_full[sub], n & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        uint32_t s[128];
+#pragma unroll
+                        for (int j = 0; j < 128; j += 32) tc::ld32(s_col + j, s + j);
+                        tc::wait_ld();
+                        const int t0 = (k.r.tile0 + k.u0 + i) << kUnitLog2;
+                        if (t0 + kUnit - 1 > sub_first || (a.window && t0 <= sub_last - a.window)) {
+                            const int hi = pos - t0, lo = a.window ? hi - a.window : -1;      // lo < key <= hi
+#pragma unroll
+                            for (int j = 0; j < 128; ++j)
+                                if (j > hi || j <= lo) s[j] = 0xff800000u;
+                        }
+                        const ChunkConst *cc = consts[kt & (kConstSets - 1)];
+                        float ym = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            float m = __uint_as_float(s[16 * j]);
+#pragma unroll
+                            for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(s[16 * j + e]));
+                            const float y = fmaf(m, fmaxf(cc[j].f * qinv, kTiny), cc[j].lb);
+                            if (m > -INFINITY) ym = fmaxf(ym, y);
+                        }
+                        if (__any_sync(kFull, ym > M + attn::kRescaleSlack)) {
+                            const float n_M = fmaxf(M, ym), r = ex2(M - n_M);
+                            M = n_M;
+                            z *= r;
+                            if (i > 0) {
+                                ok = warp_wait(&bar.o_full[sub], (n - 1) & 1);
+                                tc::fence_after();
+#pragma unroll
+                                for (int j = 0; j < D; j += 16) {
+                                    uint32_t o[16];
+                                    tc::ld16(o_col + j, o);
+                                    tc::wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                                    tc::st16(o_col + j, o);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kChunks; ++j) {
+                            const float f = fmaxf(cc[j].f * qinv, kTiny), b = cc[j].lb - M + 7.f;
+                            const uint64_t f2 = pack_f2(f, f), b2 = pack_f2(b, b);
+                            uint32_t p[8];
+                            uint64_t sum = 0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float u, v;
+                                unpack_f2(fma_f2(pack_f2(__uint_as_float(s[16 * j + 2 * e]), __uint_as_float(s[16 * j + 2 * e + 1])),
+                                                 f2, b2), u, v);
+                                u = ex2(u);
+                                v = ex2(v);
+                                sum = add_f2(sum, pack_f2(u, v));
+                                p[e] = attn::f32x2_to_f16x2(u, v);
+                            }
+                            float su, sv;
+                            unpack_f2(sum, su, sv);
+                            z = fmaf(su + sv, cc[j].iv, z);
+                            tc::st8(s_col + 8 * j, p);
+                        }
+                        tc::wait_st();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&bar.p_ready[sub]));
+                    }
+                    // ---- the row's output
+                    if (ok) ok = warp_wait(&bar.o_full[sub], (base + nu - 1) & 1);
+                    tc::fence_after();
+                    const long long first_block = k.g0 / share, last_block = (k.g0 + k.r.units - 1) / share;
+                    const int parts = (int)(last_block - first_block) + 1;
+                    if (parts == 1) {
+                        const float f = z > 0.f || z != z ? 1.f / z : 0.f;
+                        T *dst = static_cast<T *>(const_cast<void *>(a.out.p)) + (long long)(k.s.row0 + k.i0 + tok) * a.out.token +
+                                 (long long)(k.h * c.G + hd) * a.out.head;
+#pragma unroll
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t o[16];
+                            tc::ld16(o_col + j, o);
+                            tc::wait_ld();
+                            if (live && ok) {
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<uint2 *>(dst + j + e) = make_uint2(
+                                        pack2<T>(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f),
+                                        pack2<T>(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f));
+                            }
+                        }
+                    } else {
+                        const long long blk = blockIdx.x;
+                        float *p = a.part + (size_t)(2 * blk + (blk == first_block && k.g0 != blk * share)) * kPartFloats;
+                        const int r = sub * 128 + row;
+#pragma unroll
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t o[16];
+                            tc::ld16(o_col + j, o);
+                            tc::wait_ld();
+                            if (live) {
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<uint4 *>(p + 512 + r * D + j + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            }
+                        }
+                        if (live) { p[r] = M; p[256 + r] = z; }
+                        if (tid == 0 && blk == first_block) {
+                            CutItem &cut = a.cut[blk];
+                            cut.row0 = k.s.row0 + k.i0;
+                            cut.head0 = k.h * c.G;
+                            cut.tokens = tokens;
+                            cut.parts = parts;
+                            cut.second = k.g0 != blk * share;
+                        }
+                    }
+                    tc::fence_before();      // the reads of O are behind the next item's products
+                }
+                if (!ok) break;
+                n_tile += nu;
+                n_item += 1;
+                if (tokens > sub_tokens) { n_tile1 += nu; n_item1 += 1; }
+                at += nu;
+                if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
+            }
+        } else if (warp < 12) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+            // ---- codes to operands: a warp's rows are keys 32 w .. 32 w + 31 of every unit, a lane's
+            // loads row (lane / 4) of eight, 16 codes
+            const int w = warp - 8, r8 = lane >> 2, q4 = lane & 3;
+            constexpr int kHalves = D / 64, kLoads = 4 * kHalves;
+            const float sl = fabsf(a.scale_log2);
+            uint4 kr[kLoads], vr[kLoads];
+            for (;;) {
+                const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
+                const int t_item = ((k.r.tile0 + k.u0) << kUnitLog2) + 32 * w;
+                // pages and scales of the warp's two groups of 16 keys, 16 units at a time
+                int id0 = -1, id1 = -1;
+                float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
+                auto fetch = [&](int i0, int &id, float &ks, float &vs) {
+                    const int u = i0 + (lane >> 1), t = t_item + (u << kUnitLog2) + 16 * (lane & 1);
+                    id = -1;
+                    ks = vs = 0.f;
+                    if (u < nu && t < k.r.hi && t + 15 >= k.r.lo) {
+                        uint32_t bad = 0;
+                        id = load_page(c, a.block_table, k.b, t >> c.page_log2, &bad);
+                        if (id >= 0) {
+                            ks = c.k_scale[(size_t)id * c.Hkv + k.h];
+                            vs = c.v_scale[(size_t)id * c.Hkv + k.h];
+                        } else if (k.h == 0) {
+                            latch(c, bad);
+                        }
+                    }
+                };
+                fetch(0, id0, ks0, vs0);
+                fetch(16, id1, ks1, vs1);
+                // loads of unit i: eight rows an instruction
+                auto load = [&](const uint8_t *pool, int i, const int (&id)[2], uint4 (&x)[kLoads]) {
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) {
+                        const int grp = j / kHalves, half = j % kHalves, ch = grp >> 1;       // 8 rows each, two a chunk
+                        const int t = t_item + (i << kUnitLog2) + 8 * grp + r8;
+                        x[j] = make_uint4(0, 0, 0, 0);      // rows that no query sees, whatever their codes are
+                        if (id[ch] >= 0 && t >= k.r.lo && t < k.r.hi)
+                            x[j] = __ldg(reinterpret_cast<const uint4 *>(
+                                pool + ((((size_t)id[ch] * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + half * 64 + q4 * 16));
+                    }
+                };
+                auto store = [&](uint32_t dst, const uint4 (&x)[kLoads]) {
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) {
+                        const int r = 32 * w + 8 * (j / kHalves) + r8, ch = (j % kHalves) * 8 + q4 * 2;
+                        const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) code_pairs<CODE>(in[e], o[2 * e], o[2 * e + 1]);
+                        st128(dst + operand_at(r, ch), o[0], o[1], o[2], o[3]);
+                        st128(dst + operand_at(r, ch + 1), o[4], o[5], o[6], o[7]);
+                    }
+                    attn::fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                int id[2] = {__shfl_sync(kFull, id0, 0), __shfl_sync(kFull, id0, 1)};
+                load(c.k_pool, 0, id, kr);
+                load(c.v_pool, 0, id, vr);
+                for (int i = 0; i < nu && ok; ++i) {
+                    const uint32_t n = n_tile + i, st = n & 1;
+                    if (n >= 2) ok = warp_wait(&bar.k_free[st], ((n >> 1) - 1) & 1);
+                    {
+                        const float ks = __shfl_sync(kFull, ks0, 2 * (i & 15) + (lane & 1));
+                        const float vs = __shfl_sync(kFull, vs0, 2 * (i & 15) + (lane & 1));
+                        const int me = __shfl_sync(kFull, id0, 2 * (i & 15) + (lane & 1));
+                        if (lane < 2) {
+                            const float v = vs < 7.9e-31f ? 7.9e-31f : vs;        // 2^-100: its codes count for nothing
+                            consts[n & (kConstSets - 1)][2 * w + lane] =
+                                me >= 0 ? ChunkConst{ks * sl, log2f(v), 1.f / v, 0.f} : ChunkConst{0.f, -INFINITY, 0.f, 0.f};
+                        }
+                    }
+                    store(sm + L::kK + st * L::kTile, kr);
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&bar.c_full[n & (kConstSets - 1)]));
+                        mbar_arrive(smem_addr(&bar.k_full[st]));
+                    }
+                    int nid[2] = {-1, -1};
+                    if (i + 1 < nu) {
+                        if (((i + 1) & 15) == 0) {
+                            id0 = id1; ks0 = ks1; vs0 = vs1;
+                            fetch(i + 17, id1, ks1, vs1);
+                        }
+                        nid[0] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15));
+                        nid[1] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15) + 1);
+                        load(c.k_pool, i + 1, nid, kr);
+                    }
+                    if (n >= 2) ok = warp_wait(&bar.v_free[st], ((n >> 1) - 1) & 1) && ok;
+                    store(sm + L::kV + st * L::kTile, vr);
+                    if (lane == 0) mbar_arrive(smem_addr(&bar.v_full[st]));
+                    if (i + 1 < nu) load(c.v_pool, i + 1, nid, vr);
+                }
+                if (!ok) break;
+                n_tile += nu;
+                at += nu;
+                if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
+            }
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+            if (warp == 12 && lane == 0) {
+                constexpr uint32_t kIdS = tc::idesc_f16(kUnit, 0, 0), kIdO = tc::idesc_f16(D, 0, 1);
+                const uint64_t dk = tc::sdesc(0, 16, 1024), dv = tc::sdesc(0, 16384, 1024);
+                auto at_addr = [](uint64_t t, uint32_t addr) { return t | (uint64_t)((addr >> 4) & 0x3fff); };
+                auto qk = [&](int sub, uint32_t n) {
+                    const uint32_t q = sm + L::kQ + sub * L::kTile, kk = sm + L::kK + (n & 1) * L::kTile;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        tc::mma_f16(tb + kColS + 128 * sub, at_addr(dk, q + (s >> 2) * 16384 + (s & 3) * 32),
+                                    at_addr(dk, kk + (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0);
+                    tc::commit(smem_addr(&bar.s_full[sub]));
+                };
+                for (;;) {
+                    const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
+                    const int subs = min(a.tile_tokens, k.s.n - k.i0) > sub_tokens ? 2 : 1;
+                    ok = mbar_wait(smem_addr(&bar.k_full[n_tile & 1]), (n_tile >> 1) & 1);
+                    for (int s = 0; s < subs && ok; ++s) {
+                        ok = mbar_wait(smem_addr(&bar.q_ready[s]), (s ? n_item1 : n_item) & 1);
+                        tc::fence_after();
+                        if (ok) qk(s, n_tile);
+                    }
+                    if (!ok) break;
+                    tc::commit(smem_addr(&bar.k_free[n_tile & 1]));
+                    for (int i = 0; i < nu && ok; ++i) {
+                        const uint32_t n = n_tile + i;
+                        for (int s = 0; s < subs && ok; ++s) {
+                            if (s == 0) ok = mbar_wait(smem_addr(&bar.v_full[n & 1]), (n >> 1) & 1);
+                            ok = ok && mbar_wait(smem_addr(&bar.p_ready[s]), ((s ? n_tile1 : n_tile) + i) & 1);
+                            if (!ok) break;
+                            tc::fence_after();
+                            const uint32_t vv = sm + L::kV + (n & 1) * L::kTile;
+#pragma unroll
+                            for (int ks = 0; ks < kUnit / 16; ++ks)
+                                tc::mma_f16_ts(tb + kColO + 128 * s, tb + kColS + 128 * s + 8 * ks, at_addr(dv, vv + ks * 2048),
+                                               kIdO, i > 0 || ks > 0);
+                            tc::commit(smem_addr(&bar.o_full[s]));
+                            if (i + 1 < nu) {
+                                if (s == 0) ok = mbar_wait(smem_addr(&bar.k_full[(n + 1) & 1]), ((n + 1) >> 1) & 1);
+                                if (!ok) break;
+                                tc::fence_after();
+                                qk(s, n + 1);
+                            }
+                        }
+                        if (!ok) break;
+                        tc::commit(smem_addr(&bar.v_free[n & 1]));
+                        if (i + 1 < nu) tc::commit(smem_addr(&bar.k_free[(n + 1) & 1]));
+                    }
+                    if (!ok) break;
+                    n_tile += nu;
+                    n_item += 1;
+                    if (subs == 2) { n_tile1 += nu; n_item1 += 1; }
+                    at += nu;
+                    if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
+                }
+                if (!ok) {      // what was issued ends before tensor memory is given back
+                    tc::commit(smem_addr(&bar.drain));
+                    mbar_wait(smem_addr(&bar.drain), 0);
+                }
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) raise_error(c.err, kErrTimeout, kWaitTimeout);
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 12) tc::dealloc(tb, 512);
+}
+
+template <typename T, int D, int CODE>
+cudaError_t run(AttnArgs a, cudaStream_t st, int *blocks) {
+    static int occupancy[kMaxDevices];
+    const auto kernel = tiles_kernel<T, D, CODE>;
+    int sms = 0, per_sm = 0;
+    cudaError_t e = device_sm_count(&sms);
+    if (e == cudaSuccess)
+        e = cached_blocks_per_sm(occupancy, reinterpret_cast<const void *>(kernel), kThreads, Layout<D>::kBytes, &per_sm);
+    if (e != cudaSuccess) return e;
+    *blocks = min(sms, kTileBlocks);
+    kernel<<<*blocks, kThreads, Layout<D>::kBytes, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t run_type(const AttnArgs &a, cudaStream_t st, int *blocks) {
+    if (a.c.code == TKV_CODE_E4M3)
+        return a.c.D == 64 ? run<T, 64, TKV_CODE_E4M3>(a, st, blocks) : run<T, 128, TKV_CODE_E4M3>(a, st, blocks);
+    return a.c.D == 64 ? run<T, 64, TKV_CODE_INT8>(a, st, blocks) : run<T, 128, TKV_CODE_INT8>(a, st, blocks);
+}
+
+}  // namespace
+
+size_t tiles_workspace_bytes(int D) { return 2ull * kTileBlocks * 256 * (D + 2) * sizeof(float); }
+
+cudaError_t launch_tiles(AttnArgs a, cudaStream_t st, int64_t *launches) {
+    a.tile_tokens = 2 * (128 / a.c.G);
+    a.min_share = 1;
+    int blocks = 0;
+    cudaError_t e = a.c.dtype == TKV_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, st, &blocks) : run_type<__half>(a, st, &blocks);
+    if (e != cudaSuccess) return e;
+    e = launch_join(a, blocks, 256, 128, st);
+    if (e == cudaSuccess) *launches += 2;
+    return e;
+}
+
+}  // namespace paged
+}  // namespace tkv

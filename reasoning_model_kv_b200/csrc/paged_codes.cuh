@@ -1,0 +1,30 @@
+// paged_codes.cuh -- the cache's 8-bit codes as fp16 pairs (exact for both code types).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "attn_common.cuh"
+#include "tkv.h"
+
+namespace tkv {
+namespace paged {
+
+// Codes 0, 1 (lo) and 2, 3 (hi) of a word: E4M3 through the hardware's conversion, integers as
+// 0x6400 | (code + 128), which is 1024 + 128 + code in fp16, less 1152.
+template <int CODE>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (CODE == TKV_CODE_E4M3) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+        lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
+        hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 bias = attn::u32_as_h2(0x64806480u);
+        lo = attn::h2_as_u32(__hsub2(attn::u32_as_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
+        hi = attn::h2_as_u32(__hsub2(attn::u32_as_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
+    }
+}
+
+}  // namespace paged
+}  // namespace tkv

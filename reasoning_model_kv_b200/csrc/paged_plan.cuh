@@ -14,6 +14,13 @@
 namespace tkv {
 namespace paged {
 
+// The item that begins in a block's stretch and goes on in the next blocks'.
+struct CutItem {
+    int row0, head0, tokens;
+    int parts;              // blocks that hold a part; below 2: no such item
+    int second;             // the first part is the block's second partial result
+};
+
 struct AttnArgs {
     View c;
     Rows q, out;
@@ -24,6 +31,7 @@ struct AttnArgs {
     int min_share;          // units that a block takes at least
     float *part;            // [2 * blocks][rows * (D + 2)] partial results
     uint32_t *arrived;      // [blocks] blocks that have left their part of the item that begins here
+    CutItem *cut;           // [blocks]
 };
 
 // Key range of query tokens [i0, i1) of a sequence, and its tiles of `unit` keys.
