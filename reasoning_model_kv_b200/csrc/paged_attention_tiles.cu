@@ -69,6 +69,11 @@ __device__ __forceinline__ void st128(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t pack_f2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         uint32_t n_tile = 0, n_item = 0;          // units and items behind
         uint32_t n_tile1 = 0, n_item1 = 0;        // of the second tile of rows
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
             const int sub = warp >> 2, row = tid & 127;
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;
             const uint32_t s_col = tb + lanes + kColS + 128 * sub, o_col = tb + lanes + kColO + 128 * sub;
@@ -209,14 +214,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                                 if (j > hi || j <= lo) s[j] = 0xff800000u;
                         }
                         const ChunkConst *cc = consts[kt & (kConstSets - 1)];
-                        float ym = -INFINITY;
+                        float ym = -INFINITY, f[kChunks], lb[kChunks];
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
-                            float m = __uint_as_float(s[16 * j]);
+                            f[j] = fmaxf(cc[j].f * qinv, kTiny);
+                            lb[j] = cc[j].lb;
+                            float m = max3(__uint_as_float(s[16 * j]), __uint_as_float(s[16 * j + 1]), __uint_as_float(s[16 * j + 2]));
 #pragma unroll
-                            for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(s[16 * j + e]));
-                            const float y = fmaf(m, fmaxf(cc[j].f * qinv, kTiny), cc[j].lb);
-                            if (m > -INFINITY) ym = fmaxf(ym, y);
+                            for (int e = 3; e < 15; e += 2)
+                                m = max3(m, __uint_as_float(s[16 * j + e]), __uint_as_float(s[16 * j + e + 1]));
+                            m = fmaxf(m, __uint_as_float(s[16 * j + 15]));
+                            ym = fmaxf(ym, fmaf(m, f[j], lb[j]));
                         }
                         if (__any_sync(kFull, ym > M + attn::kRescaleSlack)) {
                             const float n_M = fmaxf(M, ym), r = ex2(M - n_M);
@@ -238,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         }
 #pragma unroll
                         for (int j = 0; j < kChunks; ++j) {
-                            const float f = fmaxf(cc[j].f * qinv, kTiny), b = cc[j].lb - M + 7.f;
-                            const uint64_t f2 = pack_f2(f, f), b2 = pack_f2(b, b);
+                            const float b = lb[j] - M + 7.f;
+                            const uint64_t f2 = pack_f2(f[j], f[j]), b2 = pack_f2(b, b);
                             uint32_t p[8];
                             uint64_t sum = 0;
 #pragma unroll
@@ -350,27 +358,41 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 fetch(0, id0, ks0, vs0);
                 fetch(16, id1, ks1, vs1);
                 // loads of unit i: eight rows an instruction
+                const uint32_t mine = (uint32_t)(r8 * D + q4 * 16);
                 auto load = [&](const uint8_t *pool, int i, const int (&id)[2], uint4 (&x)[kLoads]) {
+                    const int t = t_item + (i << kUnitLog2);
+                    const uint8_t *src[2];
 #pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        const int grp = j / kHalves, half = j % kHalves, ch = grp >> 1;       // 8 rows each, two a chunk
-                        const int t = t_item + (i << kUnitLog2) + 8 * grp + r8;
-                        x[j] = make_uint4(0, 0, 0, 0);      // rows that no query sees, whatever their codes are
-                        if (id[ch] >= 0 && t >= k.r.lo && t < k.r.hi)
-                            x[j] = __ldg(reinterpret_cast<const uint4 *>(
-                                pool + ((((size_t)id[ch] * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + half * 64 + q4 * 16));
+                    for (int ch = 0; ch < 2; ++ch)
+                        src[ch] = pool + ((((size_t)max(id[ch], 0) * c.Hkv + k.h) << c.page_log2) + ((t + 16 * ch) & (c.page - 1))) * D + mine;
+                    if (id[0] >= 0 && id[1] >= 0 && t >= k.r.lo && t + 32 <= k.r.hi) {
+#pragma unroll
+                        for (int j = 0; j < kLoads; ++j) {
+                            const int grp = j / kHalves, half = j % kHalves;       // eight rows each, two a chunk
+                            x[j] = __ldg(reinterpret_cast<const uint4 *>(src[grp >> 1] + (grp & 1) * 8 * D + half * 64));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kLoads; ++j) {
+                            const int grp = j / kHalves, half = j % kHalves, row = t + 8 * grp + r8;
+                            x[j] = make_uint4(0, 0, 0, 0);      // rows that no query sees, whatever their codes are
+                            if (id[grp >> 1] >= 0 && row >= k.r.lo && row < k.r.hi)
+                                x[j] = __ldg(reinterpret_cast<const uint4 *>(src[grp >> 1] + (grp & 1) * 8 * D + half * 64));
+                        }
                     }
                 };
+                const uint32_t put0 = operand_at(32 * w + r8, q4 * 2), put1 = operand_at(32 * w + r8, q4 * 2 + 1);
                 auto store = [&](uint32_t dst, const uint4 (&x)[kLoads]) {
 #pragma unroll
                     for (int j = 0; j < kLoads; ++j) {
-                        const int r = 32 * w + 8 * (j / kHalves) + r8, ch = (j % kHalves) * 8 + q4 * 2;
+                        // rows 8 on keep the exchange of chunks, and the second 64 dims are the next atom
+                        const uint32_t to = dst + (j / kHalves) * 1024 + (j % kHalves) * 16384;
                         const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
                         uint32_t o[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) code_pairs<CODE>(in[e], o[2 * e], o[2 * e + 1]);
-                        st128(dst + operand_at(r, ch), o[0], o[1], o[2], o[3]);
-                        st128(dst + operand_at(r, ch + 1), o[4], o[5], o[6], o[7]);
+                        st128(to + put0, o[0], o[1], o[2], o[3]);
+                        st128(to + put1, o[4], o[5], o[6], o[7]);
                     }
                     attn::fence_proxy_async_smem();
                     __syncwarp();
@@ -417,53 +439,67 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
             }
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-            if (warp == 12 && lane == 0) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            if (warp == 12) {
                 constexpr uint32_t kIdS = tc::idesc_f16(kUnit, 0, 0), kIdO = tc::idesc_f16(D, 0, 1);
-                const uint64_t dk = tc::sdesc(0, 16, 1024), dv = tc::sdesc(0, 16384, 1024);
-                auto at_addr = [](uint64_t t, uint32_t addr) { return t | (uint64_t)((addr >> 4) & 0x3fff); };
+                const uint64_t dk = tc::sdesc(sm, 16, 1024), dv = tc::sdesc(sm, 16384, 1024);
+                // the base is 16-byte units: offsets below 2^14 units never carry out of the field
+                auto off = [](uint64_t t, uint32_t bytes) { return t + (uint64_t)(bytes >> 4); };
                 auto qk = [&](int sub, uint32_t n) {
-                    const uint32_t q = sm + L::kQ + sub * L::kTile, kk = sm + L::kK + (n & 1) * L::kTile;
+                    const uint64_t q = off(dk, L::kQ + sub * L::kTile), kk = off(dk, L::kK + (n & 1) * L::kTile);
+                    if (tc::elect()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        tc::mma_f16(tb + kColS + 128 * sub, at_addr(dk, q + (s >> 2) * 16384 + (s & 3) * 32),
-                                    at_addr(dk, kk + (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0);
-                    tc::commit(smem_addr(&bar.s_full[sub]));
+                        for (int s = 0; s < D / 16; ++s)
+                            tc::mma_f16(tb + kColS + 128 * sub, off(q, (s >> 2) * 16384 + (s & 3) * 32),
+                                        off(kk, (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0);
+                        tc::commit(smem_addr(&bar.s_full[sub]));
+                    }
+                    __syncwarp();
+                };
+                auto pv = [&](int sub, uint32_t n, bool more) {
+                    const uint64_t vv = off(dv, L::kV + (n & 1) * L::kTile);
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int s = 0; s < kUnit / 16; ++s)
+                            tc::mma_f16_ts(tb + kColO + 128 * sub, tb + kColS + 128 * sub + 8 * s, off(vv, s * 2048), kIdO,
+                                           more || s > 0);
+                        tc::commit(smem_addr(&bar.o_full[sub]));
+                    }
+                    __syncwarp();
+                };
+                auto release = [&](uint64_t *b) {
+                    if (tc::elect()) tc::commit(smem_addr(b));
+                    __syncwarp();
                 };
                 for (;;) {
                     const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
                     const int subs = min(a.tile_tokens, k.s.n - k.i0) > sub_tokens ? 2 : 1;
-                    ok = mbar_wait(smem_addr(&bar.k_full[n_tile & 1]), (n_tile >> 1) & 1);
+                    ok = warp_wait(&bar.k_full[n_tile & 1], (n_tile >> 1) & 1);
                     for (int s = 0; s < subs && ok; ++s) {
-                        ok = mbar_wait(smem_addr(&bar.q_ready[s]), (s ? n_item1 : n_item) & 1);
+                        ok = warp_wait(&bar.q_ready[s], (s ? n_item1 : n_item) & 1);
                         tc::fence_after();
                         if (ok) qk(s, n_tile);
                     }
                     if (!ok) break;
-                    tc::commit(smem_addr(&bar.k_free[n_tile & 1]));
+                    release(&bar.k_free[n_tile & 1]);
                     for (int i = 0; i < nu && ok; ++i) {
                         const uint32_t n = n_tile + i;
                         for (int s = 0; s < subs && ok; ++s) {
-                            if (s == 0) ok = mbar_wait(smem_addr(&bar.v_full[n & 1]), (n >> 1) & 1);
-                            ok = ok && mbar_wait(smem_addr(&bar.p_ready[s]), ((s ? n_tile1 : n_tile) + i) & 1);
+                            if (s == 0) ok = warp_wait(&bar.v_full[n & 1], (n >> 1) & 1);
+                            ok = ok && warp_wait(&bar.p_ready[s], ((s ? n_tile1 : n_tile) + i) & 1);
                             if (!ok) break;
                             tc::fence_after();
-                            const uint32_t vv = sm + L::kV + (n & 1) * L::kTile;
-#pragma unroll
-                            for (int ks = 0; ks < kUnit / 16; ++ks)
-                                tc::mma_f16_ts(tb + kColO + 128 * s, tb + kColS + 128 * s + 8 * ks, at_addr(dv, vv + ks * 2048),
-                                               kIdO, i > 0 || ks > 0);
-                            tc::commit(smem_addr(&bar.o_full[s]));
+                            pv(s, n, i > 0);
                             if (i + 1 < nu) {
-                                if (s == 0) ok = mbar_wait(smem_addr(&bar.k_full[(n + 1) & 1]), ((n + 1) >> 1) & 1);
+                                if (s == 0) ok = warp_wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
                                 if (!ok) break;
                                 tc::fence_after();
                                 qk(s, n + 1);
                             }
                         }
                         if (!ok) break;
-                        tc::commit(smem_addr(&bar.v_free[n & 1]));
-                        if (i + 1 < nu) tc::commit(smem_addr(&bar.k_free[(n + 1) & 1]));
+                        release(&bar.v_free[n & 1]);
+                        if (i + 1 < nu) release(&bar.k_free[(n + 1) & 1]);
                     }
                     if (!ok) break;
                     n_tile += nu;
@@ -473,11 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
                 }
                 if (!ok) {      // what was issued ends before tensor memory is given back
-                    tc::commit(smem_addr(&bar.drain));
-                    mbar_wait(smem_addr(&bar.drain), 0);
+                    release(&bar.drain);
+                    warp_wait(&bar.drain, 0);
                 }
             }
-            __syncwarp();
         }
         if (!ok && lane == 0) raise_error(c.err, kErrTimeout, kWaitTimeout);
     }

@@ -1,8 +1,6 @@
 // paged_codes.cuh -- the cache's 8-bit codes as fp16 pairs (exact for both code types).
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "attn_common.cuh"
 #include "tkv.h"
 
@@ -14,10 +12,9 @@ namespace paged {
 template <int CODE>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (CODE == TKV_CODE_E4M3) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
-        hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = attn::u32_as_h2(0x64806480u);
