@@ -27,9 +27,7 @@ cudaError_t launch_attention(const View &c, Rows q, Rows out, int T, const int32
     a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.cut) + kCutBytes);
     const long long rows = (long long)c.G * std::min(cu ? max_q : 1, T);
     if (rows > 32) return launch_tiles(a, st, launches);
-    const cudaError_t e = launch_rows(a, rows, st);
-    if (e == cudaSuccess) ++*launches;
-    return e;
+    return launch_rows(a, rows, st, launches);
 }
 
 }  // namespace paged

@@ -14,7 +14,7 @@ constexpr int kPartRows = 160 * 64;                    // blocks * rows of an it
 // Up to 32 rows an item: keys and values from shared memory into registers, converted there,
 // warp matrix instructions (paged_attention_rows.cu).
 size_t rows_workspace_bytes(int D);
-cudaError_t launch_rows(AttnArgs a, long long rows, cudaStream_t st);
+cudaError_t launch_rows(AttnArgs a, long long rows, cudaStream_t st, int64_t *launches);
 
 // More rows: up to 256 an item, tcgen05 matrix instructions (paged_attention_tiles.cu).
 constexpr int kTileBlocks = 160;                       // blocks of its grid at most

@@ -30,7 +30,9 @@ using attn::transpose8x8;
 
 constexpr int kThreads = 128, kWarps = 4, kUnitLog2 = 6, kUnit = 64;
 constexpr int kStages = 4;
-constexpr int kChunkParts = 64;      // parts that the join holds weights of at a time
+// Parts that the last block to arrive joins by itself; more are left to the join kernel, whose
+// rows are spread over the card (one block joined 56 parts of 8 rows in 14 us, it in 3).
+constexpr int kOwnParts = 16;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_size) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_size) : "memory");
@@ -84,6 +86,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
 
     long long begin, share;
     make_plan<kThreads>(a, plan, kUnitLog2, &begin, &share);
+    if (tid == 0) a.cut[blockIdx.x].parts = 0;
     if (begin >= plan.total) return;
     const long long end = min(begin + share, plan.total);
     Cursor k;
@@ -360,7 +363,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                 if (col == 0) { p[row] = mm; p[kRows + row] = zz; }
             }
         }
-        if (parts > 1) {
+        if (parts > kOwnParts) {
+            if (tid == 0 && blockIdx.x == first_block)
+                a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts, k.g0 != first_block * share};
+        } else if (parts > 1) {
             __threadfence();
             __syncthreads();
             // the count wraps to zero with the last arrival, ready for the next call
@@ -368,60 +374,32 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-                constexpr int kPer = kRows * (D / 4) / kThreads;      // float4s of a thread
                 float *const wt = reinterpret_cast<float *>(ring_all);   // [part][row] weights
-                float *const zt = wt + kChunkParts * kRows;
-                float4 acc[kPer];
-                float mrun = attn::kNoMax, zrun = 0.f;                // of row tid (tid < kRows)
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p0 = 0; p0 < parts; p0 += kChunkParts) {
-                    const int np = min(kChunkParts, parts - p0);
-                    __syncthreads();
-                    for (int i = tid; i < np * kRows; i += kThreads) {
-                        const float *p = slot_of(first_block + p0 + i / kRows);
-                        wt[i] = __ldcg(p + i % kRows);
-                        zt[i] = __ldcg(p + kRows + i % kRows);
+                for (int i = tid; i < parts * kRows; i += kThreads) wt[i] = __ldcg(slot_of(first_block + i / kRows) + i % kRows);
+                __syncthreads();
+                if (tid < kRows) {
+                    float n = attn::kNoMax, zz = 0.f;
+                    for (int i = 0; i < parts; ++i) n = fmaxf(n, wt[i * kRows + tid]);
+                    for (int i = 0; i < parts; ++i) {
+                        const float w = ex2(wt[i * kRows + tid] - n);
+                        zz = fmaf(__ldcg(slot_of(first_block + i) + kRows + tid), w, zz);
+                        wt[i * kRows + tid] = w;
                     }
-                    __syncthreads();
-                    if (tid < kRows) {
-                        float n = mrun;
-                        for (int i = 0; i < np; ++i) n = fmaxf(n, wt[i * kRows + tid]);
-                        const float r = ex2(mrun - n);
-                        zrun *= r;
-                        for (int i = 0; i < np; ++i) {
-                            const float w = ex2(wt[i * kRows + tid] - n);
-                            zrun = fmaf(zt[i * kRows + tid], w, zrun);
-                            wt[i * kRows + tid] = w;
-                        }
-                        mrun = n;
-                        sm_m[0][tid] = r;
-                        sm_z[0][tid] = zrun;
-                    }
-                    __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const int i = j * kThreads + tid, row = i / (D / 4), col = i % (D / 4) * 4;
-                        if (row >= live_rows) continue;
-                        const float r = sm_m[0][row];
-                        acc[j].x *= r; acc[j].y *= r; acc[j].z *= r; acc[j].w *= r;
-#pragma unroll 8
-                        for (int p = 0; p < np; ++p) {
-                            const float4 u = __ldcg(reinterpret_cast<const float4 *>(
-                                slot_of(first_block + p0 + p) + 2 * kRows + row * D + col));
-                            const float w = wt[p * kRows + row];
-                            acc[j].x = fmaf(u.x, w, acc[j].x); acc[j].y = fmaf(u.y, w, acc[j].y);
-                            acc[j].z = fmaf(u.z, w, acc[j].z); acc[j].w = fmaf(u.w, w, acc[j].w);
-                        }
-                    }
+                    sm_z[0][tid] = zz > 0.f || zz != zz ? 1.f / zz : 0.f;
                 }
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int i = j * kThreads + tid, row = i / (D / 4), col = i % (D / 4) * 4;
-                    if (row >= live_rows) continue;
-                    const float zz = sm_z[0][row], f = zz > 0.f || zz != zz ? 1.f / zz : 0.f;
+                __syncthreads();
+                for (int i = tid; i < live_rows * (D / 4); i += kThreads) {
+                    const int row = i / (D / 4), col = i % (D / 4) * 4;
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int p = 0; p < parts; ++p) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(slot_of(first_block + p) + 2 * kRows + row * D + col));
+                        const float w = wt[p * kRows + row];
+                        s.x = fmaf(u.x, w, s.x); s.y = fmaf(u.y, w, s.y); s.z = fmaf(u.z, w, s.z); s.w = fmaf(u.w, w, s.w);
+                    }
+                    const float f = sm_z[0][row];
                     *reinterpret_cast<uint2 *>(out_at(row) + col) =
-                        make_uint2(pack2<T>(acc[j].x * f, acc[j].y * f), pack2<T>(acc[j].z * f, acc[j].w * f));
+                        make_uint2(pack2<T>(s.x * f, s.y * f), pack2<T>(s.z * f, s.w * f));
                 }
             }
         }
@@ -432,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
 }
 
 template <typename T, int D, int CODE, int NT>
-cudaError_t run(AttnArgs a, cudaStream_t st) {
+cudaError_t run(AttnArgs a, cudaStream_t st, int64_t *launches) {
     static int occupancy[kMaxDevices];
     const auto kernel = rows_kernel<T, D, CODE, NT>;
     int sms = 0, per_sm = 0;
@@ -444,28 +422,37 @@ cudaError_t run(AttnArgs a, cudaStream_t st) {
     a.min_share = 1;
     const int blocks = min(sms * per_sm, min(kMaxBlocks, kPartRows / (8 * NT)));
     kernel<<<blocks, kThreads, smem_bytes<D, NT>(), st>>>(a);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    ++*launches;
+    // no item has more units than the block table has room for
+    if (e == cudaSuccess && (((long long)a.c.max_pages * a.c.page + kUnit - 1) >> kUnitLog2) + 1 > kOwnParts) {
+        e = launch_join(a, blocks, 8 * NT, 8 * NT, st);
+        ++*launches;
+    }
+    return e;
 }
 template <typename T, int D, int CODE>
-cudaError_t run_rows(const AttnArgs &a, long long rows, cudaStream_t st) {
-    if (rows <= 8) return run<T, D, CODE, 1>(a, st);
-    if (rows <= 16) return run<T, D, CODE, 2>(a, st);
-    if (rows <= 24) return run<T, D, CODE, 3>(a, st);
-    return run<T, D, CODE, 4>(a, st);
+cudaError_t run_rows(const AttnArgs &a, long long rows, cudaStream_t st, int64_t *launches) {
+    if (rows <= 8) return run<T, D, CODE, 1>(a, st, launches);
+    if (rows <= 16) return run<T, D, CODE, 2>(a, st, launches);
+    if (rows <= 24) return run<T, D, CODE, 3>(a, st, launches);
+    return run<T, D, CODE, 4>(a, st, launches);
 }
 template <typename T>
-cudaError_t run_type(const AttnArgs &a, long long rows, cudaStream_t st) {
+cudaError_t run_type(const AttnArgs &a, long long rows, cudaStream_t st, int64_t *launches) {
     if (a.c.code == TKV_CODE_E4M3)
-        return a.c.D == 64 ? run_rows<T, 64, TKV_CODE_E4M3>(a, rows, st) : run_rows<T, 128, TKV_CODE_E4M3>(a, rows, st);
-    return a.c.D == 64 ? run_rows<T, 64, TKV_CODE_INT8>(a, rows, st) : run_rows<T, 128, TKV_CODE_INT8>(a, rows, st);
+        return a.c.D == 64 ? run_rows<T, 64, TKV_CODE_E4M3>(a, rows, st, launches)
+                           : run_rows<T, 128, TKV_CODE_E4M3>(a, rows, st, launches);
+    return a.c.D == 64 ? run_rows<T, 64, TKV_CODE_INT8>(a, rows, st, launches)
+                       : run_rows<T, 128, TKV_CODE_INT8>(a, rows, st, launches);
 }
 
 }  // namespace
 
 size_t rows_workspace_bytes(int D) { return 2ull * kPartRows * (D + 2) * sizeof(float); }
 
-cudaError_t launch_rows(AttnArgs a, long long rows, cudaStream_t st) {
-    return a.c.dtype == TKV_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, rows, st) : run_type<__half>(a, rows, st);
+cudaError_t launch_rows(AttnArgs a, long long rows, cudaStream_t st, int64_t *launches) {
+    return a.c.dtype == TKV_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, rows, st, launches) : run_type<__half>(a, rows, st, launches);
 }
 
 }  // namespace paged
