@@ -17,57 +17,78 @@ inline int heads_per_warp(int T, int heads) {
     return (int)(per < heads ? per : heads);
 }
 
-// Heads [h0, h1) of token t; heads from Hq on are keys.  All 32 lanes take part.
-template <typename T, int D>
-__device__ __forceinline__ void encode_rows(const tkv_rope &rope, const Rows &q, const Rows &k, const Rows &qo,
-                                            const Rows &ko, int t, int pos, int h0, int h1, int Hq) {
+// Heads [h0, h1) of one array, whose token's rows begin at in and out.  FULL: every element is
+// rotated, so no lane differs from another.
+template <typename T, int D, bool NORM, bool FULL>
+__device__ __forceinline__ void encode_heads(const tkv_rope &rope, const T *in, long long in_stride, T *out,
+                                             long long out_stride, const Row8 &w, const Angles &ang, const Chunks &c, int h0,
+                                             int h1) {
     constexpr int L = D / 8, kRows = 32 / L, kUnroll = 4;
-    const int lane = threadIdx.x & 31, j = lane & (L - 1), sub = lane / L;
-    const Chunks c = row_chunks(rope, j);
-    const T *const q0 = static_cast<const T *>(q.p) + t * q.token;
-    const T *const k0 = static_cast<const T *>(k.p) + t * k.token;
-    T *const qo0 = static_cast<T *>(const_cast<void *>(qo.p)) + t * qo.token;
-    T *const ko0 = static_cast<T *>(const_cast<void *>(ko.p)) + t * ko.token;
-    float cs[4], sn[4], qw[8], kw[8];
-    bool ready = false;
+    const int sub = (threadIdx.x & 31) / L;
+    in += (h0 + sub) * in_stride + c.a;
+    out += (h0 + sub) * out_stride + c.a;
+    const int gap = c.b - c.a;
+    int left = h1 - h0 - sub;                        // rows u of the group exist while u * kRows < left
     for (int h = h0; h < h1; h += kRows * kUnroll) {
         uint2 a[kUnroll], b[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int hh = h + u * kRows + sub;
             a[u] = b[u] = make_uint2(0, 0);
-            if (hh < h1) {
-                const T *p = hh < Hq ? q0 + hh * q.head : k0 + (hh - Hq) * k.head;
-                a[u] = *reinterpret_cast<const uint2 *>(p + c.a);
-                b[u] = *reinterpret_cast<const uint2 *>(p + c.b);
+            if (u * kRows < left) {
+                a[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride);
+                b[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride + gap);
             }
-        }
-        if (!ready) {    // behind the first loads, which it hides in part
-            double f[4];
-            load_turns(rope, j, c.turns, f);
-            load_weights<T>(rope.q_weight, c, qw);
-            load_weights<T>(rope.k_weight, c, kw);
-            turn_angles(f, pos, cs, sn);
-            ready = true;
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int hh = h + u * kRows + sub;
-            float x[8];
-            unpack8<T>(a[u], b[u], x);
-            if (rope.q_weight != nullptr) {
-                float w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = hh < Hq ? qw[i] : kw[i];
-                row_norm<D>(x, w, rope.eps);
-            }
-            if (c.turns) row_turn(x, cs, sn, rope.interleaved);
-            if (hh < h1) {
-                T *p = hh < Hq ? qo0 + hh * qo.head : ko0 + (hh - Hq) * ko.head;
-                *reinterpret_cast<uint2 *>(p + c.a) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-                *reinterpret_cast<uint2 *>(p + c.b) = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+            Row8 x = unpack8<T>(a[u], b[u]);
+            if (NORM) row_norm<D>(x, w, rope.eps);
+            if (FULL || c.turns) row_turn(x, ang, rope.interleaved);
+            if (u * kRows < left) {
+                T *p = out + u * kRows * out_stride;
+                *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(x.v[0]), pack2<T>(x.v[1]));
+                *reinterpret_cast<uint2 *>(p + gap) = make_uint2(pack2<T>(x.v[2]), pack2<T>(x.v[3]));
             }
         }
+        in += kRows * kUnroll * in_stride;
+        out += kRows * kUnroll * out_stride;
+        left -= kRows * kUnroll;
+    }
+}
+
+template <typename T, int D, bool NORM, bool FULL>
+__device__ __forceinline__ void encode_rows_as(const tkv_rope &rope, const Rows &q, const Rows &k, const Rows &qo,
+                                               const Rows &ko, int t, int pos, int h0, int h1, int Hq) {
+    const int j = threadIdx.x & (D / 8 - 1);
+    const Chunks c = row_chunks(rope, j);
+    double f[4];
+    load_turns(rope, j, FULL || c.turns, f);
+    const Angles ang = turn_angles(f, pos);
+    if (h0 < Hq) {
+        const Row8 w = NORM ? load_weights<T>(rope.q_weight, c) : Row8{};
+        encode_heads<T, D, NORM, FULL>(rope, static_cast<const T *>(q.p) + t * q.token, q.head,
+                                       static_cast<T *>(const_cast<void *>(qo.p)) + t * qo.token, qo.head, w, ang, c, h0,
+                                       min(h1, Hq));
+    }
+    if (h1 > Hq) {
+        const Row8 w = NORM ? load_weights<T>(rope.k_weight, c) : Row8{};
+        encode_heads<T, D, NORM, FULL>(rope, static_cast<const T *>(k.p) + t * k.token, k.head,
+                                       static_cast<T *>(const_cast<void *>(ko.p)) + t * ko.token, ko.head, w, ang, c,
+                                       max(h0, Hq) - Hq, h1 - Hq);
+    }
+}
+
+// Heads [h0, h1) of token t; heads from Hq on are keys.  All 32 lanes take part.
+template <typename T, int D>
+__device__ __forceinline__ void encode_rows(const tkv_rope &rope, const Rows &q, const Rows &k, const Rows &qo,
+                                            const Rows &ko, int t, int pos, int h0, int h1, int Hq) {
+    const bool full = rope.rot == D;
+    if (rope.q_weight != nullptr) {
+        if (full) encode_rows_as<T, D, true, true>(rope, q, k, qo, ko, t, pos, h0, h1, Hq);
+        else encode_rows_as<T, D, true, false>(rope, q, k, qo, ko, t, pos, h0, h1, Hq);
+    } else {
+        if (full) encode_rows_as<T, D, false, true>(rope, q, k, qo, ko, t, pos, h0, h1, Hq);
+        else encode_rows_as<T, D, false, false>(rope, q, k, qo, ko, t, pos, h0, h1, Hq);
     }
 }
 

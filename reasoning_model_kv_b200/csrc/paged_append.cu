@@ -65,7 +65,7 @@ struct AppendArgs {
     Rows k, v, q, qo;
     const int32_t *block_table, *kv_len, *cu;
     int T, max_new, slots;         // slots: pages that a sequence's new tokens can touch
-    long long units, kv_blocks;
+    uint32_t units, kv_blocks;
     int q_groups, q_per;
 };
 
@@ -76,9 +76,9 @@ template <typename T, int D, int CODE, int UT>
 __global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendArgs a) {
     constexpr int kBlock = block_threads(UT);
     const View &c = a.c;
-    if ((long long)blockIdx.x >= a.kv_blocks) {      // the queries
-        const long long w = ((long long)blockIdx.x - a.kv_blocks) * (kBlock / 32) + (threadIdx.x >> 5);
-        const int t = (int)(w / a.q_groups), lane = threadIdx.x & 31;
+    if (blockIdx.x >= a.kv_blocks) {      // the queries
+        const uint32_t w = (blockIdx.x - a.kv_blocks) * (kBlock / 32) + (threadIdx.x >> 5);
+        const int t = (int)(w / (uint32_t)a.q_groups), lane = threadIdx.x & 31;
         if (t >= a.T) return;
         int b = t;
         if (a.cu) {     // the sequence of row t: as many ends as are not behind it
@@ -91,20 +91,20 @@ __global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendA
         if (b >= c.B || !load_seq(a.cu, a.kv_len, b, a.T, &s, &bad) || t < s.row0 || t >= s.row0 + s.n ||
             s.n > a.max_new || s.len < s.n)
             return;
-        const int h0 = (int)(w - (long long)t * a.q_groups) * a.q_per;
+        const int h0 = (int)(w - (uint32_t)t * a.q_groups) * a.q_per;
         encode_rows<T, D>(a.rope, a.q, Rows{}, a.qo, Rows{}, t, s.len - s.n + (t - s.row0), h0,
                           min(h0 + a.q_per, c.Hkv * c.G), c.Hkv * c.G);
         return;
     }
     __shared__ float red[kBlock / 32];
     const int unit_in_block = threadIdx.x / UT, tid = threadIdx.x % UT;
-    const long long unit = (long long)blockIdx.x * (kBlock / UT) + unit_in_block;
+    const uint32_t unit = blockIdx.x * (kBlock / UT) + unit_in_block;
     if (unit >= a.units) return;
-    const int h = (int)(unit % c.Hkv);
-    long long rest = unit / c.Hkv;
+    uint32_t rest = unit / (uint32_t)c.Hkv;
+    const int h = (int)(unit - rest * c.Hkv);
     const bool values = rest & 1;
     rest >>= 1;
-    const int slot = (int)(rest % a.slots), b = (int)(rest / a.slots);
+    const int b = (int)(rest / (uint32_t)a.slots), slot = (int)(rest - (uint32_t)b * a.slots);
     Seq s;
     uint32_t bad = 0;
     bool ok = load_seq(a.cu, a.kv_len, b, a.T, &s, &bad);
@@ -142,30 +142,30 @@ __global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendA
     const size_t ps = (size_t)id * c.Hkv + h;
     float *const scale = (values ? c.v_scale : c.k_scale) + ps;
     const float old = lo > 0 ? *scale : 0.f;
-    float x[kPasses][8];
-    float w[8];
-    double f[4];
+    Row8 x[kPasses];
     const bool norm = !values && a.rope.k_weight != nullptr, turn = !values && ch.turns;
-    if (norm) load_weights<T>(a.rope.k_weight, ch, w);
+    Row8 w{};
+    double f[4];
+    if (norm) w = load_weights<T>(a.rope.k_weight, ch);
     load_turns(a.rope, j, turn, f);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int r = i * kRows + r0;
-        unpack8<T>(in0[i], in1[i], x[i]);
+        x[i] = unpack8<T>(in0[i], in1[i]);
         if (i * kRows < hi && (i + 1) * kRows > lo) {        // the same for all the unit's threads
             if (norm) row_norm<D>(x[i], w, a.rope.eps);
-            if (turn) {
-                float cs[4], sn[4];
-                turn_angles(f, (int)(first + r), cs, sn);
-                row_turn(x[i], cs, sn, a.rope.interleaved);
-            }
+            if (turn) row_turn(x[i], turn_angles(f, (int)(first + r)), a.rope.interleaved);
         }
         if (r >= lo && r < hi) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(x[i][e]);
-                if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);      // finite ones
+            for (int e = 0; e < 4; ++e) {
+                float u, v;
+                unpack_f2(x[i].v[e], u, v);
+                u = fabsf(u);
+                v = fabsf(v);
+                amax = fmaxf(amax, u < __int_as_float(0x7f800000) ? u : 0.f);      // finite ones
+                amax = fmaxf(amax, v < __int_as_float(0x7f800000) ? v : 0.f);
             }
         }
     }
@@ -199,7 +199,14 @@ __global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendA
         } else {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = exact ? x[i][e] * inv : x[i][e] / now;
+            for (int e = 0; e < 4; ++e) unpack_f2(x[i].v[e], y[2 * e], y[2 * e + 1]);
+            if (exact) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= inv;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] /= now;
+            }
             *c0 = codes4<CODE>(y[0], y[1], y[2], y[3]);
             *c1 = codes4<CODE>(y[4], y[5], y[6], y[7]);
         }
@@ -214,8 +221,7 @@ template <typename T, int D, int CODE, int UT>
 cudaError_t run(AppendArgs a, cudaStream_t st) {
     constexpr int kBlock = block_threads(UT);
     const long long per = kBlock / UT;
-    a.units = 2ll * a.c.B * a.slots * a.c.Hkv;
-    a.kv_blocks = (a.units + per - 1) / per;
+    const long long units = 2ll * a.c.B * a.slots * a.c.Hkv, kv_blocks = (units + per - 1) / per;
     long long q_blocks = 0;
     if (a.q.p != nullptr) {
         const int heads = a.c.Hkv * a.c.G;
@@ -223,8 +229,10 @@ cudaError_t run(AppendArgs a, cudaStream_t st) {
         a.q_groups = (heads + a.q_per - 1) / a.q_per;
         q_blocks = ((long long)a.T * a.q_groups + kBlock / 32 - 1) / (kBlock / 32);
     }
-    if (a.kv_blocks + q_blocks > INT_MAX) return cudaErrorInvalidValue;
-    append_kernel<T, D, CODE, UT><<<(unsigned)(a.kv_blocks + q_blocks), kBlock, 0, st>>>(a);
+    if (units > INT_MAX || kv_blocks + q_blocks > INT_MAX / (kBlock / 32)) return cudaErrorInvalidValue;
+    a.units = (uint32_t)units;
+    a.kv_blocks = (uint32_t)kv_blocks;
+    append_kernel<T, D, CODE, UT><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int D, int CODE>
