@@ -422,16 +422,23 @@ typedef struct {
 
 typedef struct tkv_paged tkv_paged;
 
-/* Norm and rotation of T tokens' queries [T][Hq][D] and keys [T][Hkv][D] in one pass:
- * position of token t is pos[t] (device int32).  Hq or Hkv may be 0.  Outputs may be the
- * inputs.  Returns TKV_ERR_INVALID for bad sizes, types, strides or alignment; T = 0 is a
- * no-op. */
-TKV_API tkv_status tkv_qk_norm_rope(const tkv_rope *rope, const void *q, int64_t q_token_stride,
-                                    int64_t q_head_stride, const void *k, int64_t k_token_stride,
-                                    int64_t k_head_stride, const int32_t *pos, void *q_out, void *k_out,
-                                    int64_t qo_token_stride, int64_t qo_head_stride, int64_t ko_token_stride,
-                                    int64_t ko_head_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
-                                    int32_t dtype, void *stream);
+/* A row array: address of row 0 of head 0 and its strides in elements. */
+typedef struct {
+    void *p;
+    int64_t token_stride, head_stride;
+} tkv_rows;
+
+typedef struct {
+    tkv_rows q, k, q_out, k_out;   /* [T][Hq][D] and [T][Hkv][D]                 */
+    const int32_t *pos;            /* device int32 [T]                           */
+    const tkv_rope *rope;
+    int32_t T, Hq, Hkv, D, dtype;
+} tkv_qk_norm_rope_args;
+
+/* Norm and rotation of T tokens' queries and keys in one pass: token t is at position
+ * pos[t].  Hq or Hkv may be 0.  Outputs may be the inputs.  Returns TKV_ERR_INVALID for bad
+ * sizes, types, strides or alignment; T = 0 is a no-op. */
+TKV_API tkv_status tkv_qk_norm_rope(const tkv_qk_norm_rope_args *args, void *stream);
 
 /* Bytes of device workspace a paged cache needs (0 if the configuration is invalid). */
 TKV_API size_t tkv_paged_workspace_bytes(const tkv_paged_config *cfg);
@@ -446,37 +453,45 @@ TKV_API tkv_status tkv_paged_destroy(tkv_paged *cache);
 /* Clear the workspace's counters and error word (the pools stay as they are). */
 TKV_API tkv_status tkv_paged_reset(tkv_paged *cache, void *stream);
 
+typedef struct {
+    tkv_rows k, v;                 /* [T][Hkv][D]                                */
+    tkv_rows q, q_out;             /* [T][Hkv*G][D], or both NULL                */
+    const int32_t *block_table, *kv_len, *cu;
+    const tkv_rope *rope;          /* or NULL                                    */
+    int32_t T;
+    int32_t max_new;               /* bound on a sequence's new tokens (1 .. 2^30) */
+} tkv_paged_append_args;
+
 /* Append the T rows of k and v (cu, kv_len as above; kv_len counts the new tokens), keys
  * encoded by `rope` (NULL: as they are) at their token's index in its sequence.  With
- * q != NULL the same launch writes the encoded queries [T][Hkv*G][D] to q_out.  A sequence
- * with kv_len 0 is padding: its rows are skipped, q_out's too; so are those of a sequence
- * that an error is latched for (kv_len below its number of rows: TKV_ERR_INVALID).
- *   max_new   bound on a sequence's new tokens; a sequence with more is skipped
- *             (TKV_ERR_INVALID latched)
+ * q.p != NULL the same launch writes the encoded queries to q_out.  A sequence with kv_len
+ * 0 is padding: its rows are skipped, q_out's too; so are those of a sequence that an error
+ * is latched for (kv_len below its number of rows, more than max_new rows:
+ * TKV_ERR_INVALID).
  * The scale of a page and head becomes the smallest power of two s >= 2^-64 at which every
  * finite element's magnitude is at most qmax * s (qmax 127 / 448), or stays the larger one
  * that a page with earlier tokens has; where it grows, the earlier tokens' codes are
  * rounded again to the new scale.  Codes are the fp32 value / s rounded half to even;
  * +-infinity becomes the largest code of its sign; NaN becomes E4M3 NaN, or integer 0. */
-TKV_API tkv_status tkv_paged_append(tkv_paged *cache, const tkv_rope *rope, const void *k, int64_t k_token_stride,
-                                    int64_t k_head_stride, const void *v, int64_t v_token_stride,
-                                    int64_t v_head_stride, const void *q, int64_t q_token_stride,
-                                    int64_t q_head_stride, void *q_out, int64_t qo_token_stride,
-                                    int64_t qo_head_stride, int32_t T, const int32_t *block_table,
-                                    const int32_t *kv_len, const int32_t *cu, int32_t max_new, void *stream);
+TKV_API tkv_status tkv_paged_append(tkv_paged *cache, const tkv_paged_append_args *args, void *stream);
+
+typedef struct {
+    tkv_rows q, out;               /* [T][Hkv*G][D]                              */
+    const int32_t *block_table, *kv_len, *cu;
+    int32_t T;
+    int32_t max_q;                 /* bound on a sequence's query rows (>= 1); it only
+                                      chooses the kernel                          */
+    int32_t window;                /* >= 0                                       */
+    float softmax_scale;           /* finite                                     */
+} tkv_paged_attention_args;
 
 /* GQA attention of T query rows over the cache.  Row i of the n rows of sequence b is at
  * position p = kv_len[b] - n + i and sees keys max(0, p - window + 1) .. p (window 0: all
  * keys up to p):  out = sum_j softmax_j(softmax_scale * q . k_j) v_j, rounded once; a row
- * that sees no key (one at a negative position too) gives zeros, whatever is in q.
- *   max_q     bound on a sequence's query rows; it only chooses the kernel
- *   window    >= 0
- * Tokens of a page that cannot be read (see above) count as masked. */
-TKV_API tkv_status tkv_paged_attention(tkv_paged *cache, const void *q, int64_t q_token_stride,
-                                       int64_t q_head_stride, void *out, int64_t o_token_stride,
-                                       int64_t o_head_stride, int32_t T, const int32_t *block_table,
-                                       const int32_t *kv_len, const int32_t *cu, int32_t max_q, int32_t window,
-                                       float softmax_scale, void *stream);
+ * that sees no key (one at a negative position too) gives zeros, whatever is in q.  Tokens
+ * of a page that cannot be read (see above) count as masked.  A NaN among a token's E4M3
+ * values may reach the rows of its sequence in the same call that come before it. */
+TKV_API tkv_status tkv_paged_attention(tkv_paged *cache, const tkv_paged_attention_args *args, void *stream);
 
 /* As tkv_poll_error and tkv_launch_count, for a paged cache. */
 TKV_API tkv_status tkv_paged_poll_error(tkv_paged *cache, void *stream);

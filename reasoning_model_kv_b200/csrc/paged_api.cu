@@ -51,6 +51,8 @@ const char *rope_fault(const tkv_rope *r, int D) {
     return nullptr;
 }
 
+Rows rows(const tkv_rows &r) { return {r.p, (long long)r.token_stride, (long long)r.head_stride}; }
+
 // Rows of one call: pointers and strides that eight-byte accesses can use.
 const char *rows_fault(const Rows &r) {
     if (!r.p) return "NULL row array";
@@ -92,27 +94,26 @@ size_t attention_reset_bytes();      // at the workspace's start, behind the err
 
 extern "C" {
 
-tkv_status tkv_qk_norm_rope(const tkv_rope *rope, const void *q, int64_t qt, int64_t qh, const void *k, int64_t kt,
-                            int64_t kh, const int32_t *pos, void *q_out, void *k_out, int64_t qot, int64_t qoh,
-                            int64_t kot, int64_t koh, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
-                            void *stream) {
-    if (!rope) return bad("rope is NULL");
+tkv_status tkv_qk_norm_rope(const tkv_qk_norm_rope_args *a, void *stream) {
+    if (!a || !a->rope) return bad("args or rope is NULL");
+    const int T = a->T, Hq = a->Hq, Hkv = a->Hkv, D = a->D;
     if (D != 64 && D != 128) return bad("D must be 64 or 128");
-    if (dtype != TKV_DTYPE_BF16 && dtype != TKV_DTYPE_FP16) return bad("dtype must be TKV_DTYPE_BF16 or TKV_DTYPE_FP16");
+    if (a->dtype != TKV_DTYPE_BF16 && a->dtype != TKV_DTYPE_FP16)
+        return bad("dtype must be TKV_DTYPE_BF16 or TKV_DTYPE_FP16");
     if (T < 0 || Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535) return bad("T, Hq or Hkv out of range");
-    if (const char *w = rope_fault(rope, D)) return bad(w);
+    if (const char *w = rope_fault(a->rope, D)) return bad(w);
     if (T == 0 || Hq + Hkv == 0) return TKV_OK;
-    if (!pos || !aligned(pos, 4)) return bad("pos is NULL or not 4-byte aligned");
-    Rows qr{q, qt, qh}, kr{k, kt, kh}, qor{q_out, qot, qoh}, kor{k_out, kot, koh};
+    if (!a->pos || !aligned(a->pos, 4)) return bad("pos is NULL or not 4-byte aligned");
+    const Rows q = rows(a->q), k = rows(a->k), qo = rows(a->q_out), ko = rows(a->k_out);
     if (Hq > 0) {
-        if (const char *w = rows_fault(qr)) return bad(w);
-        if (const char *w = out_fault(qor, T, Hq, D)) return bad(w);
+        if (const char *w = rows_fault(q)) return bad(w);
+        if (const char *w = out_fault(qo, T, Hq, D)) return bad(w);
     }
     if (Hkv > 0) {
-        if (const char *w = rows_fault(kr)) return bad(w);
-        if (const char *w = out_fault(kor, T, Hkv, D)) return bad(w);
+        if (const char *w = rows_fault(k)) return bad(w);
+        if (const char *w = out_fault(ko, T, Hkv, D)) return bad(w);
     }
-    return cuda_status(tkv::paged::launch_norm_rope(*rope, qr, kr, pos, qor, kor, T, Hq, Hkv, D, dtype,
+    return cuda_status(tkv::paged::launch_norm_rope(*a->rope, q, k, a->pos, qo, ko, T, Hq, Hkv, D, a->dtype,
                                                     static_cast<cudaStream_t>(stream)),
                        "tkv_qk_norm_rope");
 }
@@ -155,46 +156,44 @@ tkv_status tkv_paged_reset(tkv_paged *c, void *stream) {
     return cuda_status(cudaMemsetAsync(c->view.err, 0, 256 + tkv::paged::attention_reset_bytes(), static_cast<cudaStream_t>(stream)), "tkv_paged_reset");
 }
 
-tkv_status tkv_paged_append(tkv_paged *c, const tkv_rope *rope, const void *k, int64_t kt, int64_t kh, const void *v,
-                            int64_t vt, int64_t vh, const void *q, int64_t qt, int64_t qh, void *q_out, int64_t qot,
-                            int64_t qoh, int32_t T, const int32_t *block_table, const int32_t *kv_len,
-                            const int32_t *cu, int32_t max_new, void *stream) {
-    if (!c) return bad("cache is NULL");
-    if (const char *w = lengths_fault(c, block_table, kv_len, cu, T)) return bad(w);
+tkv_status tkv_paged_append(tkv_paged *c, const tkv_paged_append_args *a, void *stream) {
+    if (!c || !a) return bad("cache or args is NULL");
+    const int T = a->T;
+    if (const char *w = lengths_fault(c, a->block_table, a->kv_len, a->cu, T)) return bad(w);
     const tkv_rope none{};
-    const tkv_rope &r = rope ? *rope : none;
+    const tkv_rope &r = a->rope ? *a->rope : none;
     if (const char *w = rope_fault(&r, c->cfg.D)) return bad(w);
-    if (max_new < 1 || max_new > (1 << 30)) return bad("max_new must be in [1, 2^30]");
+    if (a->max_new < 1 || a->max_new > tkv::paged::kMaxLen) return bad("max_new must be in [1, 2^30]");
     if (T == 0) return TKV_OK;
-    Rows kr{k, kt, kh}, vr{v, vt, vh}, qr{q, qt, qh}, qor{q_out, qot, qoh};
-    if (const char *w = rows_fault(kr)) return bad(w);
-    if (const char *w = rows_fault(vr)) return bad(w);
-    if (q) {
-        if (const char *w = rows_fault(qr)) return bad(w);
-        if (const char *w = out_fault(qor, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
-    } else if (q_out) {
+    const Rows k = rows(a->k), v = rows(a->v), q = rows(a->q), qo = rows(a->q_out);
+    if (const char *w = rows_fault(k)) return bad(w);
+    if (const char *w = rows_fault(v)) return bad(w);
+    if (q.p) {
+        if (const char *w = rows_fault(q)) return bad(w);
+        if (const char *w = out_fault(qo, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
+    } else if (qo.p) {
         return bad("q_out without q");
     }
-    return cuda_status(tkv::paged::launch_append(c->view, r, kr, vr, qr, qor, T, block_table, kv_len, cu,
-                                                 max_new < T ? max_new : T, static_cast<cudaStream_t>(stream),
+    return cuda_status(tkv::paged::launch_append(c->view, r, k, v, q, qo, T, a->block_table, a->kv_len, a->cu,
+                                                 a->max_new < T ? a->max_new : T, static_cast<cudaStream_t>(stream),
                                                  &c->launches),
                        "tkv_paged_append");
 }
 
-tkv_status tkv_paged_attention(tkv_paged *c, const void *q, int64_t qt, int64_t qh, void *out, int64_t ot, int64_t oh,
-                               int32_t T, const int32_t *block_table, const int32_t *kv_len, const int32_t *cu,
-                               int32_t max_q, int32_t window, float softmax_scale, void *stream) {
-    if (!c) return bad("cache is NULL");
-    if (const char *w = lengths_fault(c, block_table, kv_len, cu, T)) return bad(w);
-    if (max_q < 1) return bad("max_q must be >= 1");
-    if (window < 0) return bad("window must be >= 0");
-    if (!std::isfinite(softmax_scale)) return bad("softmax_scale must be finite");
+tkv_status tkv_paged_attention(tkv_paged *c, const tkv_paged_attention_args *a, void *stream) {
+    if (!c || !a) return bad("cache or args is NULL");
+    const int T = a->T;
+    if (const char *w = lengths_fault(c, a->block_table, a->kv_len, a->cu, T)) return bad(w);
+    if (a->max_q < 1) return bad("max_q must be >= 1");
+    if (a->window < 0) return bad("window must be >= 0");
+    if (!std::isfinite(a->softmax_scale)) return bad("softmax_scale must be finite");
     if (T == 0) return TKV_OK;
-    Rows qr{q, qt, qh}, outr{out, ot, oh};
-    if (const char *w = rows_fault(qr)) return bad(w);
-    if (const char *w = out_fault(outr, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
-    return cuda_status(tkv::paged::launch_attention(c->view, qr, outr, T, block_table, kv_len, cu, max_q, window,
-                                                    softmax_scale, static_cast<cudaStream_t>(stream), &c->launches),
+    const Rows q = rows(a->q), out = rows(a->out);
+    if (const char *w = rows_fault(q)) return bad(w);
+    if (const char *w = out_fault(out, T, c->cfg.Hkv * c->cfg.G, c->cfg.D)) return bad(w);
+    return cuda_status(tkv::paged::launch_attention(c->view, q, out, T, a->block_table, a->kv_len, a->cu, a->max_q,
+                                                    a->window, a->softmax_scale, static_cast<cudaStream_t>(stream),
+                                                    &c->launches),
                        "tkv_paged_attention");
 }
 

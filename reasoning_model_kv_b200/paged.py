@@ -4,6 +4,7 @@ the current stream of the tensors' device."""
 from __future__ import annotations
 
 import ctypes
+from struct import Struct
 
 import torch
 
@@ -22,61 +23,65 @@ class TkvRopeArgs(ctypes.Structure):
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
+# The argument structs of include/tkv.h, native layout; row arrays are (address, token
+# stride, head stride).
+_NORM_ROPE_ARGS = Struct("@PqqPqqPqqPqqPPiiiii4x")
+_APPEND_ARGS = Struct("@PqqPqqPqqPqqPPPPii")
+_ATTENTION_ARGS = Struct("@PqqPqqPPPiiif")
+_NO_ROWS = (0, 0, 0)
+
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _bad(msg: str):
     raise TkvError(TKV_ERR_INVALID, msg)
 
 
-def _raw_stream(device: torch.device, stream) -> int:
-    """The stream handle of a call on tensors of `device`."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _run(device: torch.device, fn, *args):
-    """Call the library with `device` current."""
-    if device.index == torch._C._cuda_getDevice():
+def _run(index: int, fn, *args):
+    """Call the library with device `index` current."""
+    if index == _current_device():
         status = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args)
     if status:
         _check(status)
 
 
-def _rows(t: torch.Tensor, heads: int, dim: int, dtype, device, name: str):
+def _rows(t: torch.Tensor, heads: int, dim: int, dtype, index: int, name: str):
     """(address, token stride, head stride) of a [T, heads, dim] tensor."""
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        _bad(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    st = t.stride()
+    if len(st) != 3 or t.shape[1:] != (heads, dim):
+        _bad(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
     if t.dtype is not dtype:
         _bad(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        _bad(f"{name} must be on {device}, got {t.device}")
-    st = t.stride()
+    if t.get_device() != index:
+        _bad(f"{name} must be on cuda:{index}, got {t.device}")
     if st[2] != 1:
         _bad(f"{name} must have a contiguous head dim")
     return t.data_ptr(), st[0], st[1]
 
 
-def _ints(t: torch.Tensor, shape, device, name: str) -> int:
-    if t.dtype is not torch.int32:
-        _bad(f"{name} must be torch.int32, got {t.dtype}")
-    if t.device != device:
-        _bad(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        _bad(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        _bad(f"{name} must be contiguous int32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index:
+        _bad(f"{name} must be on cuda:{index}, got {t.device}")
     return t.data_ptr()
 
 
-def _output(out, shape, dtype, device, stream, name):
+def _output(out, like: torch.Tensor, stream, name: str):
+    """(out, its address and strides): a new contiguous tensor of the rows' shape, or `out`."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
         if stream is not None:
             out.record_stream(stream)
-    elif out.shape != shape:
-        _bad(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
-    return out
+        _, heads, dim = like.shape
+        return out, (out.data_ptr(), heads * dim, dim)
+    if out.shape != like.shape:
+        _bad(f"{name} must be {tuple(like.shape)}, got {tuple(out.shape)}")
+    return out, _rows(out, *like.shape[1:], like.dtype, like.get_device(), name)
 
 
 class TkvRope:
@@ -106,13 +111,13 @@ class TkvRope:
         if len(devices) > 1:
             _bad("inv_freq and the weights must be on one device")
         # what a call has to match (None: anything)
-        self.device = devices.pop() if devices else None
+        self.index = devices.pop().index if devices else None
         self.dtype = q_weight.dtype if q_weight is not None else None
         self.dim = q_weight.numel() if q_weight is not None else None
 
-    def _match(self, dtype, dim, device) -> int:
-        if self.device is not None and self.device != device:
-            _bad(f"the encoding is on {self.device}, the rows on {device}")
+    def _match(self, dtype, dim, index) -> int:
+        if self.index is not None and self.index != index:
+            _bad(f"the encoding is on cuda:{self.index}, the rows on cuda:{index}")
         if self.dtype is not None and (self.dtype is not dtype or self.dim != dim):
             _bad(f"the norm's weights are {self.dtype} [{self.dim}], the rows {dtype} [{dim}]")
         return self._ptr
@@ -125,20 +130,17 @@ def tkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: 
     may be the inputs."""
     if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
         _bad("q and k must be CUDA tensors [T, heads, D]")
-    T, Hq, D = q.shape
-    Hkv, dtype, device = k.shape[1], q.dtype, q.device
+    (T, Hq, D), Hkv, dtype, index = q.shape, k.shape[1], q.dtype, q.get_device()
     if dtype not in DTYPES:
         _bad(f"q must be bf16 or fp16, got {dtype}")
     if k.shape[0] != T:
         _bad("q and k must have the same number of tokens")
-    qr, kr = _rows(q, Hq, D, dtype, device, "q"), _rows(k, Hkv, D, dtype, device, "k")
-    p = _ints(pos, (T,), device, "pos")
-    r = rope._match(dtype, D, device)
-    q_out = _output(q_out, (T, Hq, D), dtype, device, stream, "q_out")
-    k_out = _output(k_out, (T, Hkv, D), dtype, device, stream, "k_out")
-    qo, ko = _rows(q_out, Hq, D, dtype, device, "q_out"), _rows(k_out, Hkv, D, dtype, device, "k_out")
-    _run(device, lib().tkv_qk_norm_rope, r, *qr, *kr, p, qo[0], ko[0], qo[1], qo[2], ko[1], ko[2], T, Hq, Hkv, D,
-         DTYPES[dtype], _raw_stream(device, stream))
+    qr, kr = _rows(q, Hq, D, dtype, index, "q"), _rows(k, Hkv, D, dtype, index, "k")
+    p, r = _ints(pos, (T,), index, "pos"), rope._match(dtype, D, index)
+    q_out, qo = _output(q_out, q, stream, "q_out")
+    k_out, ko = _output(k_out, k, stream, "k_out")
+    args = _NORM_ROPE_ARGS.pack(*qr, *kr, *qo, *ko, p, r, T, Hq, Hkv, D, DTYPES[dtype])
+    _run(index, lib().tkv_qk_norm_rope, args, _current_stream(index) if stream is None else stream.cuda_stream)
     return q_out, k_out
 
 
@@ -165,7 +167,7 @@ class TkvPagedCache:
             pools = (*(torch.zeros(shape, dtype=torch.uint8, device=device).view(CODES[code][1]) for _ in range(2)),
                      *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
         self.k_pool, self.v_pool, self.k_scale, self.v_scale = pools
-        self.device = self.k_pool.device
+        self.device, self.index = self.k_pool.device, self.k_pool.get_device()
         for t, want, sh, name in ((self.k_pool, CODES[code][1], shape, "k_pool"),
                                   (self.v_pool, CODES[code][1], shape, "v_pool"),
                                   (self.k_scale, torch.float32, shape[:2], "k_scale"),
@@ -190,11 +192,11 @@ class TkvPagedCache:
             lib().tkv_paged_destroy(h)
 
     def _lengths(self, block_table, kv_len, cu, T):
-        d = self.device
+        i = self.index
         if cu is None and T != self.B:
             _bad(f"without cu there is one row for each of the {self.B} sequences, got {T}")
-        return (_ints(block_table, self._table_shape, d, "block_table"), _ints(kv_len, self._len_shape, d, "kv_len"),
-                None if cu is None else _ints(cu, self._cu_shape, d, "cu"))
+        return (_ints(block_table, self._table_shape, i, "block_table"), _ints(kv_len, self._len_shape, i, "kv_len"),
+                0 if cu is None else _ints(cu, self._cu_shape, i, "cu"))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, cu=None,
                max_new: int = 1, rope: TkvRope | None = None, q=None, q_out=None, stream=None):
@@ -202,24 +204,23 @@ class TkvPagedCache:
         of sequence b, which has kv_len[b] tokens with them.  Keys are encoded by `rope` at their
         index in the sequence; with q [T, Hkv*G, D] the same launch encodes the step's queries,
         which are returned.  max_new bounds a sequence's new tokens."""
-        T, D, d = k.shape[0], self.D, self.device
-        kr = _rows(k, self.Hkv, D, self.dtype, d, "k")
-        vr = _rows(v, self.Hkv, D, self.dtype, d, "v")
+        D, index = self.D, self.index
+        kr, vr = _rows(k, self.Hkv, D, self.dtype, index, "k"), _rows(v, self.Hkv, D, self.dtype, index, "v")
+        T = k.shape[0]
         if v.shape[0] != T:
             _bad("k and v must have the same number of tokens")
-        r = None if rope is None else rope._match(self.dtype, D, d)
-        table, lens, c = self._lengths(block_table, kv_len, cu, T)
-        qr = qo = (None, 0, 0)
+        r = 0 if rope is None else rope._match(self.dtype, D, index)
+        lengths = self._lengths(block_table, kv_len, cu, T)
+        qr = qo = _NO_ROWS
         if q is not None:
-            heads = self.Hkv * self.G
-            qr = _rows(q, heads, D, self.dtype, d, "q")
+            qr = _rows(q, self.Hkv * self.G, D, self.dtype, index, "q")
             if q.shape[0] != T:
                 _bad("q and k must have the same number of tokens")
-            q_out = _output(q_out, q.shape, self.dtype, d, stream, "q_out")
-            qo = _rows(q_out, heads, D, self.dtype, d, "q_out")
+            q_out, qo = _output(q_out, q, stream, "q_out")
         elif q_out is not None:
             _bad("q_out without q")
-        _run(d, self._append, self._h, r, *kr, *vr, *qr, *qo, T, table, lens, c, max_new, _raw_stream(d, stream))
+        _run(index, self._append, self._h, _APPEND_ARGS.pack(*kr, *vr, *qr, *qo, *lengths, r, T, max_new),
+             _current_stream(index) if stream is None else stream.cuda_stream)
         return q_out
 
     def attention(self, q: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, softmax_scale: float,
@@ -228,24 +229,24 @@ class TkvPagedCache:
         last tokens of sequence b of kv_len[b].  window > 0: each sees the last `window` keys.
         max_q bounds a sequence's rows.  Rows that belong to no sequence are left as they were
         (in an output that is made here: undefined)."""
-        d, heads = self.device, self.Hkv * self.G
-        qr = _rows(q, heads, self.D, self.dtype, d, "q")
+        index = self.index
+        qr = _rows(q, self.Hkv * self.G, self.D, self.dtype, index, "q")
         T = q.shape[0]
-        table, lens, c = self._lengths(block_table, kv_len, cu, T)
-        out = _output(out, q.shape, self.dtype, d, stream, "out")
-        o = _rows(out, heads, self.D, self.dtype, d, "out")
-        _run(d, self._attention, self._h, *qr, *o, T, table, lens, c, max_q, window, softmax_scale,
-             _raw_stream(d, stream))
+        lengths = self._lengths(block_table, kv_len, cu, T)
+        out, o = _output(out, q, stream, "out")
+        _run(index, self._attention, self._h, _ATTENTION_ARGS.pack(*qr, *o, *lengths, T, max_q, window, softmax_scale),
+             _current_stream(index) if stream is None else stream.cuda_stream)
         return out
 
     def reset(self, stream=None):
         """Clear the workspace (the pools stay as they are)."""
-        _run(self.device, lib().tkv_paged_reset, self._h, _raw_stream(self.device, stream))
+        _run(self.index, lib().tkv_paged_reset, self._h,
+             _current_stream(self.index) if stream is None else stream.cuda_stream)
 
     def poll_error(self, stream=None) -> int:
         """Synchronise and return (and clear) the first device-side status."""
         with torch.cuda.device(self.device):
-            st = lib().tkv_paged_poll_error(self._h, _raw_stream(self.device, stream))
+            st = lib().tkv_paged_poll_error(self._h, _current_stream(self.index) if stream is None else stream.cuda_stream)
         if st == TKV_ERR_CUDA:
             _check(st)
         return st

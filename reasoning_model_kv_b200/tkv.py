@@ -100,23 +100,17 @@ def lib() -> ctypes.CDLL:
     L.tkv_evict_compact_window.restype = ctypes.c_int
     L.tkv_launch_count.restype = ctypes.c_int64
     L.tkv_last_error_string.restype = ctypes.c_char_p
-    i64, f32 = ctypes.c_int64, ctypes.c_float
-    rows = [vp, i64, i64]
-    L.tkv_qk_norm_rope.argtypes = [vp, *rows, *rows, vp, vp, vp, i64, i64, i64, i64, i32, i32, i32, i32, i32, vp]
-    L.tkv_qk_norm_rope.restype = ctypes.c_int
     L.tkv_paged_workspace_bytes.argtypes = [vp]
     L.tkv_paged_workspace_bytes.restype = sz
-    L.tkv_paged_create.argtypes = [vp, vp, vp, vp, vp, vp, sz, P(vp)]
-    L.tkv_paged_append.argtypes = [vp, vp, *rows, *rows, *rows, *rows, i32, vp, vp, vp, i32, vp]
-    L.tkv_paged_attention.argtypes = [vp, *rows, *rows, i32, vp, vp, vp, i32, i32, f32, vp]
-    for name, args in (("create", None), ("destroy", [vp]), ("reset", [vp, vp]), ("append", None), ("attention", None),
-                       ("poll_error", [vp, vp])):
-        fn = getattr(L, "tkv_paged_" + name)
-        fn.restype = ctypes.c_int
-        if args is not None:
-            fn.argtypes = args
+    # the calls' arguments are C structs, packed into bytes (struct.pack)
+    for name, args in (("tkv_qk_norm_rope", [ctypes.c_char_p, vp]), ("tkv_paged_destroy", [vp]),
+                       ("tkv_paged_create", [vp, vp, vp, vp, vp, vp, sz, P(vp)]), ("tkv_paged_reset", [vp, vp]),
+                       ("tkv_paged_append", [vp, ctypes.c_char_p, vp]),
+                       ("tkv_paged_attention", [vp, ctypes.c_char_p, vp]), ("tkv_paged_poll_error", [vp, vp])):
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
     L.tkv_paged_launch_count.argtypes = [vp]
-    L.tkv_paged_launch_count.restype = i64
+    L.tkv_paged_launch_count.restype = ctypes.c_int64
     for name in ("tkv_create", "tkv_destroy", "tkv_reset", "tkv_get_layout", "tkv_quantize_append",
                  "tkv_quantize_append_noalloc",
                  "tkv_decode_attention", "tkv_decode_step", "tkv_evict_compact", "tkv_poll_error", "tkv_export_state",

@@ -50,9 +50,14 @@ def test_create_refuses_bad_pointers():
     assert L.tkv_paged_create(None, *ok, ctypes.byref(h)) == INV
 
 
+KEEP = []
+
+
 def _rope(**kw):
     args = dict(inv_freq=1 << 24, rot=64, interleaved=0, q_weight=1 << 24, k_weight=1 << 24, eps=1e-6)
-    return ctypes.byref(paged.TkvRopeArgs(**{**args, **kw}))
+    r = paged.TkvRopeArgs(**{**args, **kw})
+    KEEP.append(r)
+    return ctypes.addressof(r)
 
 
 BAD_ROPES = [dict(rot=-8), dict(rot=136), dict(rot=4), dict(rot=12), dict(inv_freq=None), dict(inv_freq=(1 << 24) + 2),
@@ -65,23 +70,24 @@ def test_append_and_attention_refuse_bad_arguments_without_launching():
     row = [p, 6 * 128, 128]
     q = [p, 8 * 128, 128]
 
-    def append(rope=None, k=row, v=row, q=q, qo=q, T=2, table=p, lens=p, cu=None, max_new=1, c=h):
-        return L.tkv_paged_append(c, rope, *k, *v, *q, *qo, T, table, lens, cu, max_new, None)
+    def append(rope=0, k=row, v=row, q=q, qo=q, T=2, table=p, lens=p, cu=0, max_new=1, c=h):
+        return L.tkv_paged_append(c, paged._APPEND_ARGS.pack(*k, *v, *q, *qo, table, lens, cu, rope, T, max_new), None)
 
-    def attend(q=q, o=q, T=2, table=p, lens=p, cu=None, max_q=1, window=0, scale=0.1, c=h):
-        return L.tkv_paged_attention(c, *q, *o, T, table, lens, cu, max_q, window, scale, None)
+    def attend(q=q, o=q, T=2, table=p, lens=p, cu=0, max_q=1, window=0, scale=0.1, c=h):
+        return L.tkv_paged_attention(c, paged._ATTENTION_ARGS.pack(*q, *o, table, lens, cu, T, max_q, window, scale), None)
 
-    bad_rows = ([None, 768, 128], [p + 4, 768, 128], [p, 770, 128], [p, 768, 126], [p, -768, 128], [p, 768, -4])
+    bad_rows = ([0, 768, 128], [p + 4, 768, 128], [p, 770, 128], [p, 768, 126], [p, -768, 128], [p, 768, -4])
     overlap = ([p, 0, 128], [p, 8 * 128, 64], [p, 64, 128])
-    common = (dict(T=-1), dict(T=3), dict(table=None), dict(lens=None), dict(table=p + 2), dict(lens=p + 1), dict(cu=p + 2),
+    common = (dict(T=-1), dict(T=3), dict(table=0), dict(lens=0), dict(table=p + 2), dict(lens=p + 1), dict(cu=p + 2),
               dict(c=None))
     for kw in (*common, dict(max_new=0), dict(max_new=-1), dict(max_new=(1 << 30) + 1), *(dict(k=r) for r in bad_rows),
                *(dict(v=r) for r in bad_rows), *(dict(q=r) for r in bad_rows[1:]), *(dict(qo=r) for r in bad_rows),
-               *(dict(qo=r) for r in overlap), dict(q=[None, 0, 0]), *(dict(rope=_rope(**r)) for r in BAD_ROPES)):
+               *(dict(qo=r) for r in overlap), dict(q=[0, 0, 0]), *(dict(rope=_rope(**r)) for r in BAD_ROPES)):
         assert append(**kw) == INV, kw
     for kw in (*common, dict(max_q=0), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")),
                *(dict(q=r) for r in bad_rows), *(dict(o=r) for r in bad_rows), *(dict(o=r) for r in overlap)):
         assert attend(**kw) == INV, kw
+    assert L.tkv_paged_append(h, None, None) == INV and L.tkv_paged_attention(h, None, None) == INV
     assert append(T=0, cu=p) == 0 and attend(T=0, cu=p) == 0           # no rows: no-op
     assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_launch_count(None) == 0
     assert L.tkv_paged_reset(None, None) == INV and L.tkv_paged_poll_error(None, None) == INV
@@ -93,10 +99,11 @@ def test_norm_rope_refuses_bad_arguments_without_launching():
 
     def call(rope=_rope(), q=(p, 1024, 128), k=(p, 256, 128), pos=p, qo=p, ko=p, qs=(1024, 128), ks=(256, 128), T=4, Hq=8,
              Hkv=2, D=128, dtype=0):
-        return L.tkv_qk_norm_rope(rope, *q, *k, pos, qo, ko, *qs, *ks, T, Hq, Hkv, D, dtype, None)
+        return L.tkv_qk_norm_rope(paged._NORM_ROPE_ARGS.pack(*q, *k, qo, *qs, ko, *ks, pos, rope, T, Hq, Hkv, D, dtype), None)
 
-    for kw in (dict(rope=None), dict(pos=None), dict(pos=p + 2), dict(T=-1), dict(Hq=-1), dict(Hkv=-1), dict(Hq=65536),
-               dict(D=96), dict(dtype=2), dict(qo=None), dict(ko=None), dict(qo=p + 4), dict(qs=(64, 128)),
+    assert L.tkv_qk_norm_rope(None, None) == INV
+    for kw in (dict(rope=0), dict(pos=0), dict(pos=p + 2), dict(T=-1), dict(Hq=-1), dict(Hkv=-1), dict(Hq=65536),
+               dict(D=96), dict(dtype=2), dict(qo=0), dict(ko=0), dict(qo=p + 4), dict(qs=(64, 128)),
                dict(qs=(1024, 64)), dict(ks=(256, 0)), dict(q=(p, 1022, 128)), dict(k=(p + 2, 256, 128)),
                dict(k=(p, 256, -128)), *(dict(rope=_rope(**r)) for r in BAD_ROPES)):
         assert call(**kw) == INV, kw
