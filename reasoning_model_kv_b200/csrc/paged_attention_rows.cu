@@ -30,6 +30,8 @@ using attn::transpose8x8;
 
 constexpr int kThreads = 128, kWarps = 4, kUnitLog2 = 6, kUnit = 64;
 constexpr int kStages = 4;
+// An item's setup takes about as long as this many units.
+constexpr int kItemCost = 7;
 // Parts that the last block to arrive joins by itself; more are left to the join kernel, whose
 // rows are spread over the card (one block joined 56 parts of 8 rows in 14 us, it in 3).
 constexpr int kOwnParts = 16;
@@ -91,10 +93,66 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
     const long long end = min(begin + share, plan.total);
     Cursor k;
     cursor_start(a, plan, begin, kUnitLog2, &k);
-    long long at = begin;
-    for (;;) {
-        const int nu = (int)min((long long)(k.r.units - k.u0), end - at);      // units of this item
+    do {
+        int u0, nu;
+        cursor_units(k, begin, end, &u0, &nu);
+        if (nu == 0) continue;
         const int tokens = min(a.tile_tokens, k.s.n - k.i0);
+        // ---- the warp's 16 keys of every unit
+        const int tok0 = ((k.r.tile0 + u0) << kUnitLog2) + warp * 16;         // first key of the first unit
+        // Pages and scales of 32 units at a time, a lane each, the next 32 in flight.
+        int id0 = -1, id1 = -1;
+        float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
+        auto fetch = [&](int i0, int &id, float &ks, float &vs) {
+            const int t = tok0 + ((i0 + lane) << kUnitLog2);
+            id = -1;
+            ks = vs = 0.f;
+            if (i0 + lane < nu && t < k.r.hi && t + 15 >= k.r.lo) {
+                uint32_t bad = 0;
+                id = load_page(c, a.block_table, k.b, t >> c.page_log2, &bad);
+                if (id >= 0) {
+                    ks = c.k_scale[(size_t)id * c.Hkv + k.h];
+                    vs = c.v_scale[(size_t)id * c.Hkv + k.h];
+                } else if (k.h == 0) {
+                    latch(c, bad);
+                }
+            }
+        };
+        fetch(0, id0, ks0, vs0);
+        fetch(32, id1, ks1, vs1);
+        // The copies of unit i's keys and values, and what its products need of the page.
+        auto copy = [&](int i) {
+            if (i < nu) {
+                if ((i & 31) == 0 && i > 0) {
+                    id0 = id1; ks0 = ks1; vs0 = vs1;
+                    fetch(i + 32, id1, ks1, vs1);
+                }
+                const int id = __shfl_sync(kFull, id0, i & 31);
+                const int st = i % kStages, t = tok0 + (i << kUnitLog2);
+                const size_t base =
+                    ((((size_t)max(id, 0) * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + lane * 16;
+                const uint32_t dst = ring + st * kStageBytes;
+#pragma unroll
+                for (int j = 0; j < kTile / 512; ++j) {
+                    const int r = (j * 512 + lane * 16) / D, ch = (lane * 16 % D) >> 4;
+                    // rows that no query sees are zeros, whatever their codes are
+                    const uint32_t n = id >= 0 && t + r >= k.r.lo && t + r < k.r.hi ? 16 : 0;
+                    cp_async16(dst + chunk_at<D>(r, ch), c.k_pool + base + j * 512, n);
+                    cp_async16(dst + kTile + chunk_at<D>(r, ch), c.v_pool + base + j * 512, n);
+                }
+            }
+            attn::cp_async_commit();
+        };
+        auto note = [&](int i) {
+            if (i < nu) {
+                const int id = __shfl_sync(kFull, id0, i & 31);
+                const float ks = __shfl_sync(kFull, ks0, i & 31), vs = __shfl_sync(kFull, vs0, i & 31);
+                if (lane == 0) stage_info[warp][i % kStages] = Stage{ks, vs, id >= 0, 0};
+            }
+        };
+        // the first copies go out before the queries are read and before the scales are there
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy(i);
         // ---- the queries, as B fragments (column g of every tile of eight rows)
         uint32_t qf[NT][kSteps][2];
         float qinv[NT][2];
@@ -137,7 +195,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             qinv[nt][0] = __shfl_sync(kFull, inv, 8 * tig);
             qinv[nt][1] = __shfl_sync(kFull, inv, 8 * tig + 4);
         }
-        // ---- the warp's 16 keys of every unit
         float o[NT][kSteps][4], m[NT][2], z[NT][2], vref = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -146,56 +203,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
         }
-        const int tok0 = ((k.r.tile0 + k.u0) << kUnitLog2) + warp * 16;         // first key of the first unit
         const int last_pos = k.r.first + tokens - 1;
-        // Pages and scales of 32 units at a time, a lane each, the next 32 in flight.
-        int id0 = -1, id1 = -1;
-        float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
-        auto fetch = [&](int i0, int &id, float &ks, float &vs) {
-            const int t = tok0 + ((i0 + lane) << kUnitLog2);
-            id = -1;
-            ks = vs = 0.f;
-            if (i0 + lane < nu && t < k.r.hi && t + 15 >= k.r.lo) {
-                uint32_t bad = 0;
-                id = load_page(c, a.block_table, k.b, t >> c.page_log2, &bad);
-                if (id >= 0) {
-                    ks = c.k_scale[(size_t)id * c.Hkv + k.h];
-                    vs = c.v_scale[(size_t)id * c.Hkv + k.h];
-                } else if (k.h == 0) {
-                    latch(c, bad);
-                }
-            }
-        };
-        fetch(0, id0, ks0, vs0);
-        fetch(32, id1, ks1, vs1);
-        auto issue = [&](int i) {
-            if (i < nu) {
-                if ((i & 31) == 0 && i > 0) {
-                    id0 = id1; ks0 = ks1; vs0 = vs1;
-                    fetch(i + 32, id1, ks1, vs1);
-                }
-                const int id = __shfl_sync(kFull, id0, i & 31);
-                const float ks = __shfl_sync(kFull, ks0, i & 31), vs = __shfl_sync(kFull, vs0, i & 31);
-                const int st = i % kStages, t = tok0 + (i << kUnitLog2);
-                if (lane == 0) stage_info[warp][st] = Stage{ks, vs, id >= 0, 0};
-                const size_t base =
-                    ((((size_t)max(id, 0) * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + lane * 16;
-                const uint32_t dst = ring + st * kStageBytes;
 #pragma unroll
-                for (int j = 0; j < kTile / 512; ++j) {
-                    const int r = (j * 512 + lane * 16) / D, ch = (lane * 16 % D) >> 4;
-                    // rows that no query sees are zeros, whatever their codes are
-                    const uint32_t n = id >= 0 && t + r >= k.r.lo && t + r < k.r.hi ? 16 : 0;
-                    cp_async16(dst + chunk_at<D>(r, ch), c.k_pool + base + j * 512, n);
-                    cp_async16(dst + kTile + chunk_at<D>(r, ch), c.v_pool + base + j * 512, n);
-                }
-            }
-            attn::cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        for (int i = 0; i < kStages - 1; ++i) note(i);
         for (int i = 0; i < nu; ++i) {
-            issue(i + kStages - 1);
+            copy(i + kStages - 1);
+            note(i + kStages - 1);
             cp_async_wait<kStages - 1>();
             __syncwarp();
             const int st = i % kStages, t = tok0 + (i << kUnitLog2);
@@ -329,16 +342,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                                                                            o[nt][s + 1][e] * f, o[nt][s + 1][e + 2] * f);
             }
         __syncthreads();
-        const long long first_block = k.g0 / share, last_block = (k.g0 + k.r.units - 1) / share;
-        const int parts = (int)(last_block - first_block) + 1;
+        const Parts cut = item_parts(k, share);
+        const int parts = cut.count;
         auto out_at = [&](int row) {
             const int ti = row / c.G;
             return static_cast<T *>(const_cast<void *>(a.out.p)) + (long long)(k.s.row0 + k.i0 + ti) * a.out.token +
                    (long long)(k.h * c.G + row - ti * c.G) * a.out.head;
         };
-        auto slot_of = [&](long long blk) {
-            return a.part + (size_t)(2 * blk + (blk == first_block && k.g0 != blk * share)) * kPartFloats;
-        };
+        auto slot_of = [&](long long blk) { return part_at(a, kPartFloats, cut.first, blk); };
         const int live_rows = tokens * c.G;
         for (int i = tid; i < kRows * (D / 4); i += kThreads) {
             const int row = i / (D / 4), col = i % (D / 4) * 4;
@@ -364,25 +375,25 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             }
         }
         if (parts > kOwnParts) {
-            if (tid == 0 && blockIdx.x == first_block)
-                a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts, k.g0 != first_block * share};
+            if (tid == 0 && blockIdx.x == cut.first)
+                a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts};
         } else if (parts > 1) {
             __threadfence();
             __syncthreads();
             // the count wraps to zero with the last arrival, ready for the next call
-            if (tid == 0) sm_last = atomicInc(a.arrived + first_block, parts - 1) == (uint32_t)parts - 1;
+            if (tid == 0) sm_last = atomicInc(a.arrived + cut.first, parts - 1) == (uint32_t)parts - 1;
             __syncthreads();
             if (sm_last) {
                 __threadfence();
                 float *const wt = reinterpret_cast<float *>(ring_all);   // [part][row] weights
-                for (int i = tid; i < parts * kRows; i += kThreads) wt[i] = __ldcg(slot_of(first_block + i / kRows) + i % kRows);
+                for (int i = tid; i < parts * kRows; i += kThreads) wt[i] = __ldcg(slot_of(cut.first + i / kRows) + i % kRows);
                 __syncthreads();
                 if (tid < kRows) {
                     float n = attn::kNoMax, zz = 0.f;
                     for (int i = 0; i < parts; ++i) n = fmaxf(n, wt[i * kRows + tid]);
                     for (int i = 0; i < parts; ++i) {
                         const float w = ex2(wt[i * kRows + tid] - n);
-                        zz = fmaf(__ldcg(slot_of(first_block + i) + kRows + tid), w, zz);
+                        zz = fmaf(__ldcg(slot_of(cut.first + i) + kRows + tid), w, zz);
                         wt[i * kRows + tid] = w;
                     }
                     sm_z[0][tid] = zz > 0.f || zz != zz ? 1.f / zz : 0.f;
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
                     for (int p = 0; p < parts; ++p) {
-                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(slot_of(first_block + p) + 2 * kRows + row * D + col));
+                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(slot_of(cut.first + p) + 2 * kRows + row * D + col));
                         const float w = wt[p * kRows + row];
                         s.x = fmaf(u.x, w, s.x); s.y = fmaf(u.y, w, s.y); s.z = fmaf(u.z, w, s.z); s.w = fmaf(u.w, w, s.w);
                     }
@@ -403,10 +414,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                 }
             }
         }
-        at += nu;
-        if (at >= end || !cursor_next(a, kUnitLog2, &k)) return;
         __syncthreads();        // the ring and the join's arrays are free
-    }
+    } while (cursor_next(a, kUnitLog2, end, &k));
 }
 
 template <typename T, int D, int CODE, int NT>
@@ -419,7 +428,7 @@ cudaError_t run(AttnArgs a, cudaStream_t st, int64_t *launches) {
                                                    smem_bytes<D, NT>(), &per_sm);
     if (e != cudaSuccess) return e;
     a.tile_tokens = 8 * NT / a.c.G;
-    a.min_share = 1;
+    a.item_cost = kItemCost;
     const int blocks = min(sms * per_sm, min(kMaxBlocks, kPartRows / (8 * NT)));
     kernel<<<blocks, kThreads, smem_bytes<D, NT>(), st>>>(a);
     e = cudaGetLastError();

@@ -32,6 +32,7 @@ using attn::mbar_wait;
 using attn::smem_addr;
 
 constexpr int kThreads = 512, kUnitLog2 = 7, kUnit = 128;
+constexpr int kItemCost = 2;             // an item's setup takes about as long as this many units
 constexpr int kChunks = kUnit / 16;      // groups of keys that share a page
 constexpr int kConstSets = 4;
 constexpr float kTiny = 1e-37f;          // factors of logits stay above zero: -inf times one is -inf
@@ -118,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     } else {
         Cursor k;
         cursor_start(a, plan, begin, kUnitLog2, &k);
-        long long at = begin;
         uint32_t n_tile = 0, n_item = 0;          // units and items behind
         uint32_t n_tile1 = 0, n_item1 = 0;        // of the second tile of rows
         if (warp < 8) {
@@ -128,8 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             const uint32_t s_col = tb + lanes + kColS + 128 * sub, o_col = tb + lanes + kColO + 128 * sub;
             const int ti = row / c.G, hd = row - ti * c.G;
             if (tid == 0 && a.cut) a.cut[blockIdx.x].parts = 0;
-            for (;;) {
-                const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
+            do {
+                int u0, nu;
+                cursor_units(k, begin, end, &u0, &nu);
+                if (nu == 0) continue;
                 const int tokens = min(a.tile_tokens, k.s.n - k.i0);
                 if (sub == 0 || tokens > sub_tokens) {
                     const int tok = sub * sub_tokens + ti;
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
                         for (int j = 0; j < 128; j += 32) tc::ld32(s_col + j, s + j);
                         tc::wait_ld();
-                        const int t0 = (k.r.tile0 + k.u0 + i) << kUnitLog2;
+                        const int t0 = (k.r.tile0 + u0 + i) << kUnitLog2;
                         if (t0 + kUnit - 1 > sub_first || (a.window && t0 <= sub_last - a.window)) {
                             const int hi = pos - t0, lo = a.window ? hi - a.window : -1;      // lo < key <= hi
 #pragma unroll
@@ -255,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     // ---- the row's output
                     if (ok) ok = warp_wait(&bar.o_full[sub], (base + nu - 1) & 1);
                     tc::fence_after();
-                    const long long first_block = k.g0 / share, last_block = (k.g0 + k.r.units - 1) / share;
-                    const int parts = (int)(last_block - first_block) + 1;
+                    const Parts cut = item_parts(k, share);
+                    const int parts = cut.count;
                     if (parts == 1) {
                         const float f = z > 0.f || z != z ? 1.f / z : 0.f;
                         T *dst = static_cast<T *>(const_cast<void *>(a.out.p)) + (long long)(k.s.row0 + k.i0 + tok) * a.out.token +
@@ -275,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             }
                         }
                     } else {
-                        const long long blk = blockIdx.x;
-                        float *p = a.part + (size_t)(2 * blk + (blk == first_block && k.g0 != blk * share)) * kPartFloats;
+                        float *p = part_at(a, kPartFloats, cut.first, blockIdx.x);
                         const int r = sub * 128 + row;
 #pragma unroll
                         for (int j = 0; j < D; j += 16) {
@@ -290,14 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             }
                         }
                         if (live) { p[r] = M; p[256 + r] = z; }
-                        if (tid == 0 && blk == first_block) {
-                            CutItem &cut = a.cut[blk];
-                            cut.row0 = k.s.row0 + k.i0;
-                            cut.head0 = k.h * c.G;
-                            cut.tokens = tokens;
-                            cut.parts = parts;
-                            cut.second = k.g0 != blk * share;
-                        }
+                        if (tid == 0 && blockIdx.x == cut.first)
+                            a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts};
                     }
                     tc::fence_before();      // the reads of O are behind the next item's products
                 }
@@ -305,9 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 n_tile += nu;
                 n_item += 1;
                 if (tokens > sub_tokens) { n_tile1 += nu; n_item1 += 1; }
-                at += nu;
-                if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
-            }
+            } while (cursor_next(a, kUnitLog2, end, &k));
         } else if (warp < 12) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
             // ---- codes to operands: a warp's rows are keys 32 w .. 32 w + 31 of every unit, a lane's
@@ -316,9 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             constexpr int kHalves = D / 64, kLoads = 4 * kHalves;
             const float sl = fabsf(a.scale_log2);
             uint4 kr[kLoads], vr[kLoads];
-            for (;;) {
-                const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
-                const int t_item = ((k.r.tile0 + k.u0) << kUnitLog2) + 32 * w;
+            do {
+                int u0, nu;
+                cursor_units(k, begin, end, &u0, &nu);
+                if (nu == 0) continue;
+                const int t_item = ((k.r.tile0 + u0) << kUnitLog2) + 32 * w;
                 // pages and scales of the warp's two groups of 16 keys, 16 units at a time
                 int id0 = -1, id1 = -1;
                 float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
@@ -417,9 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 }
                 if (!ok) break;
                 n_tile += nu;
-                at += nu;
-                if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
-            }
+            } while (cursor_next(a, kUnitLog2, end, &k));
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
             if (warp == 12) {
@@ -453,8 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     if (tc::elect()) tc::commit(smem_addr(b));
                     __syncwarp();
                 };
-                for (;;) {
-                    const int nu = (int)min((long long)(k.r.units - k.u0), end - at);
+                do {
+                    int u0, nu;
+                    cursor_units(k, begin, end, &u0, &nu);
+                    if (nu == 0) continue;
                     const int subs = min(a.tile_tokens, k.s.n - k.i0) > sub_tokens ? 2 : 1;
                     ok = warp_wait(&bar.k_full[n_tile & 1], (n_tile >> 1) & 1);
                     for (int s = 0; s < subs && ok; ++s) {
@@ -487,9 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     n_tile += nu;
                     n_item += 1;
                     if (subs == 2) { n_tile1 += nu; n_item1 += 1; }
-                    at += nu;
-                    if (at >= end || !cursor_next(a, kUnitLog2, &k)) break;
-                }
+                } while (cursor_next(a, kUnitLog2, end, &k));
                 if (!ok) {      // what was issued ends before tensor memory is given back
                     release(&bar.drain);
                     warp_wait(&bar.drain, 0);
@@ -530,7 +523,7 @@ size_t tiles_workspace_bytes(int D) { return 2ull * kTileBlocks * 256 * (D + 2) 
 
 cudaError_t launch_tiles(AttnArgs a, cudaStream_t st, int64_t *launches) {
     a.tile_tokens = 2 * (128 / a.c.G);
-    a.min_share = 1;
+    a.item_cost = kItemCost;
     int blocks = 0;
     cudaError_t e = a.c.dtype == TKV_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, st, &blocks) : run_type<__half>(a, st, &blocks);
     if (e != cudaSuccess) return e;

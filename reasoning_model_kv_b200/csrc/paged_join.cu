@@ -28,8 +28,7 @@ __global__ void __launch_bounds__(32 * kWarps) join_kernel(const AttnArgs a, int
     const int tok = i / G, hd = i - tok * G, per = tile_rows / G;
     const int r = tok / per * tile_rows + (tok % per) * G + hd;
     const size_t stride = (size_t)item_rows * (D + 2);
-    const float *const mine = a.part + 2 * (size_t)blk * stride;
-    auto part = [&](int p) { return mine + (p == 0 ? (size_t)cut.second : 2 * (size_t)p) * stride; };
+    auto part = [&](int p) { return part_at(a, stride, blk, blk + p); };
     float M = attn::kNoMax, z = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;

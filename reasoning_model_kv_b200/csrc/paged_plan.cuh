@@ -3,9 +3,10 @@
 // An item is one (sequence, kv head, tile of query tokens); its units are the tiles of keys
 // that its rows can see, at least one.  All items' units lie on one line, sequence by
 // sequence, and every block takes an equal stretch of it: ragged lengths, long sequences and
-// small batches all end up balanced without the host knowing a length.  An item that is cut
-// leaves partial results (running maximum, sum, unnormalised output), and the block that
-// arrives last joins them in block order, so results do not depend on the order of arrival.
+// small batches all end up balanced without the host knowing a length.  Before its units an
+// item has `item_cost` places on the line that stand for its setup (queries, page table, first
+// copies, output).  An item whose units are cut leaves partial results (running maximum, sum,
+// unnormalised output), which are joined in block order whichever block arrives last.
 #pragma once
 
 #include "attn_common.cuh"
@@ -18,7 +19,6 @@ namespace paged {
 struct CutItem {
     int row0, head0, tokens;
     int parts;              // blocks that hold a part; below 2: no such item
-    int second;             // the first part is the block's second partial result
 };
 
 struct AttnArgs {
@@ -28,8 +28,9 @@ struct AttnArgs {
     int T, window;
     float scale_log2;       // softmax_scale * log2(e)
     int tile_tokens;        // query tokens of an item
-    int min_share;          // units that a block takes at least
-    float *part;            // [2 * blocks][rows * (D + 2)] partial results
+    int item_cost;          // an item's setup in units
+    float *part;            // [blocks][2][rows * (D + 2)] partial results: of the item that a
+                            // block goes on with, of the one that it begins
     uint32_t *arrived;      // [blocks] blocks that have left their part of the item that begins here
     CutItem *cut;           // [blocks]
 };
@@ -37,7 +38,7 @@ struct AttnArgs {
 // Key range of query tokens [i0, i1) of a sequence, and its tiles of `unit` keys.
 struct KeyRange {
     int first, lo, hi;      // position of token i0; keys [lo, hi) are seen by some row
-    int tile0, units;
+    int tile0, units;       // units >= 1
 };
 __device__ __forceinline__ KeyRange key_range(const AttnArgs &a, const Seq &s, int i0, int unit_log2) {
     KeyRange r;
@@ -48,6 +49,12 @@ __device__ __forceinline__ KeyRange key_range(const AttnArgs &a, const Seq &s, i
     r.tile0 = r.lo >> unit_log2;
     r.units = max(1, ((r.hi + (1 << unit_log2) - 1) >> unit_log2) - r.tile0);
     return r;
+}
+
+// a / b for a >= 0, b > 0; nearly always in 32 bits, whose division is a fifth as long.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+    return (long long)((uint32_t)a / (uint32_t)b);
 }
 
 // A sequence's rows and length for attention: n = 0 where the rows cannot be used, len = 0
@@ -69,10 +76,10 @@ struct Plan {
     long long off;          // units of that sequence before it
 };
 
-// Units of one kv head of sequence s.
+// Places of one kv head of sequence s on the line.
 __device__ __forceinline__ long long head_units(const AttnArgs &a, const Seq &s, int unit_log2) {
     long long u = 0;
-    for (int i0 = 0; i0 < s.n; i0 += a.tile_tokens) u += key_range(a, s, i0, unit_log2).units;
+    for (int i0 = 0; i0 < s.n; i0 += a.tile_tokens) u += a.item_cost + key_range(a, s, i0, unit_log2).units;
     return u;
 }
 
@@ -92,7 +99,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warp_sum
     return v;
 }
 
-// Finds the block's stretch: *share units from *begin on (none if begin >= total), and where
+// Finds the block's stretch: *share places from *begin on (none if begin >= total), and where
 // that is.  Block 0 reports sequences that cannot be used.  All NT threads take part.
 template <int NT>
 __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_log2, long long *begin, long long *share) {
@@ -109,7 +116,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_l
     if (tid == NT - 1) p.total = incl;
     __syncthreads();
     const long long total = p.total;
-    *share = max((total + gridDim.x - 1) / gridDim.x, (long long)a.min_share);
+    *share = quotient(total + gridDim.x - 1, gridDim.x);
     *begin = *share * blockIdx.x;
     if (B <= NT) {
         if (tid < B && *begin >= incl - sum && *begin < incl) { p.b = tid; p.off = *begin - (incl - sum); }
@@ -136,31 +143,35 @@ struct Cursor {
     int b, h, i0;           // sequence, kv head, first query token
     Seq s;
     KeyRange r;
-    int u0;                 // first unit of the item that is this block's
-    long long g0;           // the item's first unit on the line
+    long long g0;           // the item's first unit on the line (behind its setup)
 };
+// Units [u0, u0 + nu) of the cursor's item are in the stretch [begin, end); nu may be 0.
+__device__ __forceinline__ void cursor_units(const Cursor &k, long long begin, long long end, int *u0, int *nu) {
+    const long long lo = max(begin - k.g0, 0ll), hi = min(end - k.g0, (long long)k.r.units);
+    *u0 = (int)lo;
+    *nu = (int)max(hi - lo, 0ll);
+}
 
 __device__ __forceinline__ void cursor_start(const AttnArgs &a, const Plan &p, long long begin, int unit_log2, Cursor *k) {
     uint32_t bad;
     k->b = p.b;
     k->s = attention_seq(a, k->b, &bad);
     const long long per = head_units(a, k->s, unit_log2);
-    k->h = (int)(p.off / per);
+    k->h = (int)quotient(p.off, per);
     long long off = p.off - k->h * per;
     k->i0 = 0;
     for (;;) {
         k->r = key_range(a, k->s, k->i0, unit_log2);
-        if (off < k->r.units) break;
-        off -= k->r.units;
+        if (off < a.item_cost + k->r.units) break;
+        off -= a.item_cost + k->r.units;
         k->i0 += a.tile_tokens;
     }
-    k->u0 = (int)off;
-    k->g0 = begin - off;
+    k->g0 = begin - off + a.item_cost;
 }
-// The next item; false behind the last one.
-__device__ __forceinline__ bool cursor_next(const AttnArgs &a, int unit_log2, Cursor *k) {
-    k->g0 += k->r.units;
-    k->u0 = 0;
+// The next item; false behind the last one and behind the stretch's end.
+__device__ __forceinline__ bool cursor_next(const AttnArgs &a, int unit_log2, long long end, Cursor *k) {
+    k->g0 += k->r.units + a.item_cost;
+    if (k->g0 >= end) return false;
     k->i0 += a.tile_tokens;
     if (k->i0 >= k->s.n) {
         k->i0 = 0;
@@ -175,6 +186,20 @@ __device__ __forceinline__ bool cursor_next(const AttnArgs &a, int unit_log2, Cu
     }
     k->r = key_range(a, k->s, k->i0, unit_log2);
     return true;
+}
+
+// The blocks whose stretches hold units of the cursor's item, and where block blk's partial
+// result of it is.
+struct Parts {
+    long long first;
+    int count;
+};
+__device__ __forceinline__ Parts item_parts(const Cursor &k, long long share) {
+    const long long first = quotient(k.g0, share);
+    return {first, (int)(quotient(k.g0 + k.r.units - 1, share) - first) + 1};
+}
+__device__ __forceinline__ float *part_at(const AttnArgs &a, size_t floats, long long first, long long blk) {
+    return a.part + (size_t)(2 * blk + (blk == first)) * floats;
 }
 
 }  // namespace paged

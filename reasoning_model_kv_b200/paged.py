@@ -8,6 +8,7 @@ from struct import Struct
 
 import torch
 
+from . import tkv
 from .tkv import TKV_ERR_CUDA, TKV_ERR_INVALID, TkvError, _check, lib
 
 CODES = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
@@ -187,9 +188,10 @@ class TkvPagedCache:
         torch.cuda.current_stream(self.device).synchronize()    # ready for any stream
 
     def __del__(self):
-        h, self._h = getattr(self, "_h", None), None
-        if h is not None:
-            lib().tkv_paged_destroy(h)
+        h = getattr(self, "_h", None)
+        if h is not None and tkv._lib is not None:
+            tkv._lib.tkv_paged_destroy(h)
+            self._h = None
 
     def _lengths(self, block_table, kv_len, cu, T):
         i = self.index
