@@ -31,7 +31,7 @@ using attn::transpose8x8;
 constexpr int kThreads = 128, kWarps = 4, kUnitLog2 = 6, kUnit = 64;
 constexpr int kStages = 4;
 // An item's setup takes about as long as this many units.
-constexpr int kItemCost = 7;
+constexpr int kItemCost = 4;
 // Parts that the last block to arrive joins by itself; more are left to the join kernel, whose
 // rows are spread over the card (one block joined 56 parts of 8 rows in 14 us, it in 3).
 constexpr int kOwnParts = 16;

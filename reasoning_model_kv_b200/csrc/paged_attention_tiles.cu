@@ -76,7 +76,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-template <typename T, int D, int CODE>
+// SETS: constants of a unit that the softmax reads, one for every 64 keys (pages of 64 tokens or
+// more) or every 16.
+template <typename T, int D, int CODE, int SETS>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ AttnArgs a) {
     using L = Layout<D>;
     constexpr int kPartFloats = 256 * (D + 2);
@@ -182,8 +184,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     const uint32_t base = sub ? n_tile1 : n_tile;       // tiles of this half before the item
                     for (int i = 0; i < nu && ok; ++i) {
                         const uint32_t n = base + i, kt = n_tile + i;
-                        ok = warp_wait(&bar.c_full[kt & (kConstSets - 1)], (kt / kConstSets) & 1) &&
-                             warp_wait(&bar.s_full[sub], n & 1);
+                        ok = warp_wait(&bar.c_full[kt & (kConstSets - 1)], (kt / kConstSets) & 1);
+                        // read while S is formed: with eight reads behind it a unit took an eighth longer
+                        const ChunkConst *cc = consts[kt & (kConstSets - 1)];
+                        constexpr int kKeys = kUnit / SETS;
+                        float f[SETS], lb[SETS];
+#pragma unroll
+                        for (int j = 0; j < SETS; ++j) {
+                            const ChunkConst w = cc[j * (kKeys / 16)];
+                            f[j] = fmaxf(w.f * qinv, kTiny);
+                            lb[j] = w.lb;
+                        }
+                        ok = ok && warp_wait(&bar.s_full[sub], n & 1);
                         if (!ok) break;
                         tc::fence_after();
                         uint32_t s[128];
@@ -197,18 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             for (int j = 0; j < 128; ++j)
                                 if (j > hi || j <= lo) s[j] = 0xff800000u;
                         }
-                        const ChunkConst *cc = consts[kt & (kConstSets - 1)];
-                        float ym = -INFINITY, f[kChunks], lb[kChunks];
+                        float ym = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < kChunks; ++j) {
-                            f[j] = fmaxf(cc[j].f * qinv, kTiny);
-                            lb[j] = cc[j].lb;
-                            float m = max3(__uint_as_float(s[16 * j]), __uint_as_float(s[16 * j + 1]), __uint_as_float(s[16 * j + 2]));
+                        for (int j = 0; j < SETS; ++j) {
+                            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int e = 3; e < 15; e += 2)
-                                m = max3(m, __uint_as_float(s[16 * j + e]), __uint_as_float(s[16 * j + e + 1]));
-                            m = fmaxf(m, __uint_as_float(s[16 * j + 15]));
-                            ym = fmaxf(ym, fmaf(m, f[j], lb[j]));
+                            for (int e = 0; e < kKeys; e += 2)
+                                m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[kKeys * j + e]), __uint_as_float(s[kKeys * j + e + 1]));
+                            ym = fmaxf(ym, fmaf(fmaxf(max3(m[0], m[1], m[2]), m[3]), f[j], lb[j]));
                         }
                         if (__any_sync(kFull, ym > M + attn::kRescaleSlack)) {
                             const float n_M = fmaxf(M, ym), r = ex2(M - n_M);
@@ -229,25 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < kChunks; ++j) {
+                        for (int j = 0; j < SETS; ++j) {
                             const float b = lb[j] - M + 7.f;
                             const uint64_t f2 = pack_f2(f[j], f[j]), b2 = pack_f2(b, b);
-                            uint32_t p[8];
-                            uint64_t sum = 0;
+                            uint64_t sum[2] = {0, 0};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float u, v;
-                                unpack_f2(fma_f2(pack_f2(__uint_as_float(s[16 * j + 2 * e]), __uint_as_float(s[16 * j + 2 * e + 1])),
-                                                 f2, b2), u, v);
-                                u = ex2(u);
-                                v = ex2(v);
-                                sum = add_f2(sum, pack_f2(u, v));
-                                p[e] = attn::f32x2_to_f16x2(u, v);
+                            for (int q = 0; q < kKeys; q += 16) {
+                                uint32_t p[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int at = kKeys * j + q + 2 * e;
+                                    float u, v;
+                                    unpack_f2(fma_f2(pack_f2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), f2, b2), u, v);
+                                    u = ex2(u);
+                                    v = ex2(v);
+                                    sum[e & 1] = add_f2(sum[e & 1], pack_f2(u, v));
+                                    p[e] = attn::f32x2_to_f16x2(u, v);
+                                }
+                                tc::st8(s_col + (kKeys * j + q) / 2, p);
                             }
                             float su, sv;
-                            unpack_f2(sum, su, sv);
-                            z = fmaf(su + sv, cc[j].iv, z);
-                            tc::st8(s_col + 8 * j, p);
+                            unpack_f2(add_f2(sum[0], sum[1]), su, sv);
+                            z = fmaf(su + sv, cc[j * (kKeys / 16)].iv, z);
                         }
                         tc::wait_st();
                         tc::fence_before();
@@ -374,41 +385,45 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     attn::fence_proxy_async_smem();
                     __syncwarp();
                 };
-                int id[2] = {__shfl_sync(kFull, id0, 0), __shfl_sync(kFull, id0, 1)};
-                load(c.k_pool, 0, id, kr);
-                load(c.v_pool, 0, id, vr);
-                for (int i = 0; i < nu && ok; ++i) {
+                ChunkConst cc0;
+                auto constants = [&] {
+                    const float v = fmaxf(vs0, 7.9e-31f);        // 2^-100: its codes count for nothing
+                    cc0 = id0 >= 0 ? ChunkConst{ks0 * sl, log2f(v), 1.f / v, 0.f} : ChunkConst{0.f, -INFINITY, 0.f, 0.f};
+                };
+                int idk[2] = {__shfl_sync(kFull, id0, 0), __shfl_sync(kFull, id0, 1)};
+                load(c.k_pool, 0, idk, kr);
+                load(c.v_pool, 0, idk, vr);
+                constants();
+                // keys run one unit ahead of values: unit i's products wait for its keys first
+                auto put_keys = [&](int i) {
                     const uint32_t n = n_tile + i, st = n & 1;
                     if (n >= 2) ok = warp_wait(&bar.k_free[st], ((n >> 1) - 1) & 1);
-                    {
-                        const float ks = __shfl_sync(kFull, ks0, 2 * (i & 15) + (lane & 1));
-                        const float vs = __shfl_sync(kFull, vs0, 2 * (i & 15) + (lane & 1));
-                        const int me = __shfl_sync(kFull, id0, 2 * (i & 15) + (lane & 1));
-                        if (lane < 2) {
-                            const float v = vs < 7.9e-31f ? 7.9e-31f : vs;        // 2^-100: its codes count for nothing
-                            consts[n & (kConstSets - 1)][2 * w + lane] =
-                                me >= 0 ? ChunkConst{ks * sl, log2f(v), 1.f / v, 0.f} : ChunkConst{0.f, -INFINITY, 0.f, 0.f};
-                        }
-                    }
+                    if ((lane >> 1) == (i & 15)) consts[n & (kConstSets - 1)][2 * w + (lane & 1)] = cc0;
                     store(sm + L::kK + st * L::kTile, kr);
                     if (lane == 0) {
                         mbar_arrive(smem_addr(&bar.c_full[n & (kConstSets - 1)]));
                         mbar_arrive(smem_addr(&bar.k_full[st]));
                     }
-                    int nid[2] = {-1, -1};
                     if (i + 1 < nu) {
                         if (((i + 1) & 15) == 0) {
                             id0 = id1; ks0 = ks1; vs0 = vs1;
                             fetch(i + 17, id1, ks1, vs1);
+                            constants();
                         }
-                        nid[0] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15));
-                        nid[1] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15) + 1);
-                        load(c.k_pool, i + 1, nid, kr);
+                        idk[0] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15));
+                        idk[1] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15) + 1);
+                        load(c.k_pool, i + 1, idk, kr);
                     }
+                };
+                put_keys(0);
+                for (int i = 0; i < nu && ok; ++i) {
+                    const int idn[2] = {idk[0], idk[1]};                 // of unit i + 1
+                    if (i + 1 < nu) put_keys(i + 1);
+                    const uint32_t n = n_tile + i, st = n & 1;
                     if (n >= 2) ok = warp_wait(&bar.v_free[st], ((n >> 1) - 1) & 1) && ok;
                     store(sm + L::kV + st * L::kTile, vr);
                     if (lane == 0) mbar_arrive(smem_addr(&bar.v_full[st]));
-                    if (i + 1 < nu) load(c.v_pool, i + 1, nid, vr);
+                    if (i + 1 < nu) load(c.v_pool, i + 1, idn, vr);
                 }
                 if (!ok) break;
                 n_tile += nu;
@@ -426,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s)
                             tc::mma_f16(tb + kColS + 128 * sub, off(q, (s >> 2) * 16384 + (s & 3) * 32),
-                                        off(kk, (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0);
-                        tc::commit(smem_addr(&bar.s_full[sub]));
+                                        off(kk, (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0, 1);
+                        tc::commit(smem_addr(&bar.s_full[sub]), 1);
                     }
                     __syncwarp();
                 };
@@ -437,13 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
                         for (int s = 0; s < kUnit / 16; ++s)
                             tc::mma_f16_ts(tb + kColO + 128 * sub, tb + kColS + 128 * sub + 8 * s, off(vv, s * 2048), kIdO,
-                                           more || s > 0);
-                        tc::commit(smem_addr(&bar.o_full[sub]));
+                                           more || s > 0, 1);
+                        tc::commit(smem_addr(&bar.o_full[sub]), 1);
                     }
                     __syncwarp();
                 };
                 auto release = [&](uint64_t *b) {
-                    if (tc::elect()) tc::commit(smem_addr(b));
+                    if (tc::elect()) tc::commit(smem_addr(b), 1);
                     __syncwarp();
                 };
                 do {
@@ -461,21 +476,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     release(&bar.k_free[n_tile & 1]);
                     for (int i = 0; i < nu && ok; ++i) {
                         const uint32_t n = n_tile + i;
+                        ok = warp_wait(&bar.v_full[n & 1], (n >> 1) & 1);
+                        if (i + 1 < nu) ok = ok && warp_wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
                         for (int s = 0; s < subs && ok; ++s) {
-                            if (s == 0) ok = warp_wait(&bar.v_full[n & 1], (n >> 1) & 1);
                             ok = ok && warp_wait(&bar.p_ready[s], ((s ? n_tile1 : n_tile) + i) & 1);
                             if (!ok) break;
                             tc::fence_after();
                             pv(s, n, i > 0);
+                            if (s == subs - 1) release(&bar.v_free[n & 1]);
                             if (i + 1 < nu) {
-                                if (s == 0) ok = warp_wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                                if (!ok) break;
-                                tc::fence_after();
                                 qk(s, n + 1);
                             }
                         }
                         if (!ok) break;
-                        release(&bar.v_free[n & 1]);
                         if (i + 1 < nu) release(&bar.k_free[(n + 1) & 1]);
                     }
                     if (!ok) break;
@@ -497,10 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (warp == 12) tc::dealloc(tb, 512);
 }
 
-template <typename T, int D, int CODE>
+template <typename T, int D, int CODE, int SETS>
 cudaError_t run(AttnArgs a, cudaStream_t st, int *blocks) {
     static int occupancy[kMaxDevices];
-    const auto kernel = tiles_kernel<T, D, CODE>;
+    const auto kernel = tiles_kernel<T, D, CODE, SETS>;
     int sms = 0, per_sm = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e == cudaSuccess)
@@ -510,11 +523,15 @@ cudaError_t run(AttnArgs a, cudaStream_t st, int *blocks) {
     kernel<<<*blocks, kThreads, Layout<D>::kBytes, st>>>(a);
     return cudaGetLastError();
 }
+template <typename T, int D, int CODE>
+cudaError_t run_page(const AttnArgs &a, cudaStream_t st, int *blocks) {
+    return a.c.page >= 64 ? run<T, D, CODE, 2>(a, st, blocks) : run<T, D, CODE, 8>(a, st, blocks);
+}
 template <typename T>
 cudaError_t run_type(const AttnArgs &a, cudaStream_t st, int *blocks) {
     if (a.c.code == TKV_CODE_E4M3)
-        return a.c.D == 64 ? run<T, 64, TKV_CODE_E4M3>(a, st, blocks) : run<T, 128, TKV_CODE_E4M3>(a, st, blocks);
-    return a.c.D == 64 ? run<T, 64, TKV_CODE_INT8>(a, st, blocks) : run<T, 128, TKV_CODE_INT8>(a, st, blocks);
+        return a.c.D == 64 ? run_page<T, 64, TKV_CODE_E4M3>(a, st, blocks) : run_page<T, 128, TKV_CODE_E4M3>(a, st, blocks);
+    return a.c.D == 64 ? run_page<T, 64, TKV_CODE_INT8>(a, st, blocks) : run_page<T, 128, TKV_CODE_INT8>(a, st, blocks);
 }
 
 }  // namespace
