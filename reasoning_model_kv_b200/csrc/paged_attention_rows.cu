@@ -36,7 +36,10 @@ constexpr int kItemCost = 4;
 // rows are spread over the card (one block joined 56 parts of 8 rows in 14 us, it in 3).
 constexpr int kOwnParts = 16;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_size) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, uint32_t src_size) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_size) : "memory");
 }
 template <int N>
@@ -86,6 +89,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
     const uint32_t ring = smem_addr(ring_all) + warp * kStages * kStageBytes;
 
+    // where the lane's chunk of a copy of 512 bytes goes; four rows of 128 bytes on, the exchange
+    // of chunks differs in one bit
+    const uint32_t lane_at = chunk_at<D>(lane * 16 / D, lane * 16 % D >> 4);
+    const uint32_t lane_flip = D == 128 ? (lane_at ^ 64) - lane_at : 0;
+
     long long begin, share;
     make_plan<kThreads>(a, plan, kUnitLog2, &begin, &share);
     if (tid == 0) a.cut[blockIdx.x].parts = 0;
@@ -129,16 +137,24 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                 }
                 const int id = __shfl_sync(kFull, id0, i & 31);
                 const int st = i % kStages, t = tok0 + (i << kUnitLog2);
-                const size_t base =
-                    ((((size_t)max(id, 0) * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + lane * 16;
-                const uint32_t dst = ring + st * kStageBytes;
+                const size_t base = ((((size_t)max(id, 0) * c.Hkv + k.h) << c.page_log2) + (t & (c.page - 1))) * D + lane * 16;
+                const uint8_t *const ks = c.k_pool + base, *const vs = c.v_pool + base;
+                const uint32_t dst = ring + st * kStageBytes + lane_at, dst2 = dst + lane_flip;
+                if (id >= 0 && t >= k.r.lo && t + 16 <= k.r.hi) {
 #pragma unroll
-                for (int j = 0; j < kTile / 512; ++j) {
-                    const int r = (j * 512 + lane * 16) / D, ch = (lane * 16 % D) >> 4;
-                    // rows that no query sees are zeros, whatever their codes are
-                    const uint32_t n = id >= 0 && t + r >= k.r.lo && t + r < k.r.hi ? 16 : 0;
-                    cp_async16(dst + chunk_at<D>(r, ch), c.k_pool + base + j * 512, n);
-                    cp_async16(dst + kTile + chunk_at<D>(r, ch), c.v_pool + base + j * 512, n);
+                    for (int j = 0; j < kTile / 512; ++j) {
+                        cp_async16((j & 1 ? dst2 : dst) + j * 512, ks + j * 512);
+                        cp_async16((j & 1 ? dst2 : dst) + j * 512 + kTile, vs + j * 512);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kTile / 512; ++j) {
+                        // rows that no query sees are zeros, whatever their codes are
+                        const int r = t + (j * 512 + lane * 16) / D;
+                        const uint32_t n = id >= 0 && r >= k.r.lo && r < k.r.hi ? 16 : 0;
+                        cp_async16_or_zero((j & 1 ? dst2 : dst) + j * 512, ks + j * 512, n);
+                        cp_async16_or_zero((j & 1 ? dst2 : dst) + j * 512 + kTile, vs + j * 512, n);
+                    }
                 }
             }
             attn::cp_async_commit();
