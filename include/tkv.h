@@ -371,7 +371,7 @@ TKV_API int64_t tkv_launch_count(const tkv_cache *cache);
  *   k_pool, v_pool    8-bit [pages][Hkv][page][D]
  *   k_scale, v_scale  fp32  [pages][Hkv]            value = code * scale
  * Codes are signed integers in [-127, 127] (code 0) or FP8 E4M3 (code 1).  Scales are
- * finite and >= 0; the append writes powers of two.  Token j of sequence b is in page
+ * 0 or finite and >= 2^-80; the append writes powers of two from 2^-64 on.  Token j of sequence b is in page
  * block_table[b * max_pages + j / page], slot j % page.  A page that an append writes
  * belongs to one sequence; pages that are only read may be shared.
  *
@@ -445,7 +445,8 @@ TKV_API size_t tkv_paged_workspace_bytes(const tkv_paged_config *cfg);
 
 /* Create a paged cache over the caller's pools (16-byte aligned), scales and workspace
  * (256-byte aligned, at least tkv_paged_workspace_bytes(cfg) bytes).  The device is not
- * touched: call tkv_paged_reset once before the first use. */
+ * touched: call tkv_paged_reset once before the first use.  Caches whose calls follow one
+ * another on one stream may share a workspace (and then an error word). */
 TKV_API tkv_status tkv_paged_create(const tkv_paged_config *cfg, void *k_pool, void *v_pool, float *k_scale,
                                     float *v_scale, void *d_workspace, size_t workspace_bytes, tkv_paged **out);
 TKV_API tkv_status tkv_paged_destroy(tkv_paged *cache);

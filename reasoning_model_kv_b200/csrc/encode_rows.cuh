@@ -17,42 +17,57 @@ inline int heads_per_warp(int T, int heads) {
     return (int)(per < heads ? per : heads);
 }
 
+// A group of up to kUnroll warp-fuls of rows; WHOLE: all of them are there.
+template <typename T, int D, bool NORM, bool FULL, bool WHOLE>
+__device__ __forceinline__ void encode_group(const tkv_rope &rope, const T *in, long long in_stride, T *out,
+                                             long long out_stride, const Row8 &w, const Angles &ang, const Chunks &c,
+                                             int left) {
+    constexpr int kRows = 256 / D, kUnroll = 4;
+    const int gap = c.b - c.a;
+    uint2 a[kUnroll], b[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        if (!WHOLE) a[u] = b[u] = make_uint2(0, 0);
+        if (WHOLE || u * kRows < left) {
+            a[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride);
+            b[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride + gap);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        Row8 x = unpack8<T>(a[u], b[u]);
+        if (NORM) row_norm<D>(x, w, rope.eps);
+        if (FULL || c.turns) row_turn(x, ang, rope.interleaved);
+        if (WHOLE || u * kRows < left) {
+            T *p = out + u * kRows * out_stride;
+            *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(x.v[0]), pack2<T>(x.v[1]));
+            *reinterpret_cast<uint2 *>(p + gap) = make_uint2(pack2<T>(x.v[2]), pack2<T>(x.v[3]));
+        }
+    }
+}
+
 // Heads [h0, h1) of one array, whose token's rows begin at in and out.  FULL: every element is
 // rotated, so no lane differs from another.
 template <typename T, int D, bool NORM, bool FULL>
 __device__ __forceinline__ void encode_heads(const tkv_rope &rope, const T *in, long long in_stride, T *out,
                                              long long out_stride, const Row8 &w, const Angles &ang, const Chunks &c, int h0,
                                              int h1) {
-    constexpr int L = D / 8, kRows = 32 / L, kUnroll = 4;
+    constexpr int L = D / 8, kRows = 32 / L, kGroup = 4 * kRows;
     const int sub = (threadIdx.x & 31) / L;
     in += (h0 + sub) * in_stride + c.a;
     out += (h0 + sub) * out_stride + c.a;
-    const int gap = c.b - c.a;
-    int left = h1 - h0 - sub;                        // rows u of the group exist while u * kRows < left
-    for (int h = h0; h < h1; h += kRows * kUnroll) {
-        uint2 a[kUnroll], b[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            a[u] = b[u] = make_uint2(0, 0);
-            if (u * kRows < left) {
-                a[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride);
-                b[u] = *reinterpret_cast<const uint2 *>(in + u * kRows * in_stride + gap);
-            }
+    int h = h0;
+    if (in_stride == D && out_stride == D) {       // heads side by side: offsets are constants
+        for (; h + kGroup <= h1; h += kGroup) {
+            encode_group<T, D, NORM, FULL, true>(rope, in, D, out, D, w, ang, c, 0);
+            in += kGroup * D;
+            out += kGroup * D;
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            Row8 x = unpack8<T>(a[u], b[u]);
-            if (NORM) row_norm<D>(x, w, rope.eps);
-            if (FULL || c.turns) row_turn(x, ang, rope.interleaved);
-            if (u * kRows < left) {
-                T *p = out + u * kRows * out_stride;
-                *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(x.v[0]), pack2<T>(x.v[1]));
-                *reinterpret_cast<uint2 *>(p + gap) = make_uint2(pack2<T>(x.v[2]), pack2<T>(x.v[3]));
-            }
-        }
-        in += kRows * kUnroll * in_stride;
-        out += kRows * kUnroll * out_stride;
-        left -= kRows * kUnroll;
+    }
+    for (; h < h1; h += kGroup) {
+        encode_group<T, D, NORM, FULL, false>(rope, in, in_stride, out, out_stride, w, ang, c, h1 - h - sub);
+        in += kGroup * in_stride;
+        out += kGroup * out_stride;
     }
 }
 

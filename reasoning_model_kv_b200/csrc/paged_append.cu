@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "encode_rows.cuh"
+#include "paged_plan.cuh"
 
 namespace tkv {
 namespace paged {
@@ -66,14 +67,26 @@ struct AppendArgs {
     const int32_t *block_table, *kv_len, *cu;
     int T, max_new, slots;         // slots: pages that a sequence's new tokens can touch
     uint32_t units, kv_blocks;
+    bool compact;                  // units are numbered over the pages that are touched
     int q_groups, q_per;
 };
+
+// The rows and length of sequence b; false for padding (*bad 0) and where they cannot be used.
+__device__ __forceinline__ bool append_seq(const AppendArgs &a, int b, Seq *s, uint32_t *bad) {
+    if (!load_seq(a.cu, a.kv_len, b, a.T, s, bad)) return false;
+    if (s->len == 0) return false;
+    if (s->n > a.max_new) *bad = kBadRows;
+    else if (s->len < s->n) *bad = kBadLen;
+    return *bad == 0;
+}
 
 // Threads of a unit (UT = page * D / 32) and of a block.
 __host__ __device__ constexpr int block_threads(int ut) { return ut > 256 ? ut : 256; }
 
+// Four blocks an SM (64 registers, a few spilled): the units wait for memory and for each other,
+// and with three blocks eight prompt chunks took 109 us for 99.
 template <typename T, int D, int CODE, int UT>
-__global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(block_threads(UT), UT > 256 ? 2 : 4) append_kernel(const AppendArgs a) {
     constexpr int kBlock = block_threads(UT);
     const View &c = a.c;
     if (blockIdx.x >= a.kv_blocks) {      // the queries
@@ -86,33 +99,64 @@ __global__ void __launch_bounds__(block_threads(UT)) append_kernel(const AppendA
             for (int i = 0; i < c.B; i += 32) b += __popc(__ballot_sync(0xffffffffu, i + lane < c.B && a.cu[i + lane + 1] <= t));
         }
         Seq s;
-        uint32_t bad;
+        uint32_t bad = 0;
         // what is wrong with a sequence is reported by its keys' units
-        if (b >= c.B || !load_seq(a.cu, a.kv_len, b, a.T, &s, &bad) || t < s.row0 || t >= s.row0 + s.n ||
-            s.n > a.max_new || s.len < s.n)
-            return;
+        if (b >= c.B || !append_seq(a, b, &s, &bad) || t < s.row0 || t >= s.row0 + s.n) return;
         const int h0 = (int)(w - (uint32_t)t * a.q_groups) * a.q_per;
         encode_rows<T, D>(a.rope, a.q, Rows{}, a.qo, Rows{}, t, s.len - s.n + (t - s.row0), h0,
                           min(h0 + a.q_per, c.Hkv * c.G), c.Hkv * c.G);
         return;
     }
     __shared__ float red[kBlock / 32];
+    constexpr int kUnits = kBlock / UT;
     const int unit_in_block = threadIdx.x / UT, tid = threadIdx.x % UT;
-    const uint32_t unit = blockIdx.x * (kBlock / UT) + unit_in_block;
-    if (unit >= a.units) return;
-    uint32_t rest = unit / (uint32_t)c.Hkv;
-    const int h = (int)(unit - rest * c.Hkv);
-    const bool values = rest & 1;
-    rest >>= 1;
-    const int b = (int)(rest / (uint32_t)a.slots), slot = (int)(rest - (uint32_t)b * a.slots);
+    const uint32_t unit = blockIdx.x * kUnits + unit_in_block;
+    const uint32_t nth = unit / (uint32_t)c.Hkv;              // key or value pages before it
+    const int h = (int)(unit - nth * c.Hkv);
+    const bool values = nth & 1;
+    int b, slot;
+    if (a.compact) {
+        // One sequence is far longer than most: the page that the unit's number stands for, counted
+        // over the sequences.
+        __shared__ long long warp_sum[kBlock / 32], behind;
+        __shared__ int at[kUnits][2];
+        if (threadIdx.x < kUnits) at[threadIdx.x][0] = -1;
+        const long long first = blockIdx.x * kUnits / (2 * (uint32_t)c.Hkv);
+        const long long last = (blockIdx.x * kUnits + kUnits - 1) / (2 * (uint32_t)c.Hkv);
+        long long before = 0;
+        for (int b0 = 0; b0 < c.B && (before <= last || blockIdx.x == 0); b0 += kBlock) {
+            const int mine = b0 + threadIdx.x;
+            long long pages = 0;
+            if (mine < c.B) {
+                Seq s;
+                uint32_t bad = 0;
+                if (append_seq(a, mine, &s, &bad) && s.n > 0)
+                    pages = ((s.len - 1) >> c.page_log2) - ((s.len - s.n) >> c.page_log2) + 1;
+                if (bad && blockIdx.x == 0) latch(c, bad);
+            }
+            const long long end = before + block_scan<kBlock>(pages, warp_sum);
+            for (int u = 0; u < kUnits; ++u) {
+                const long long j = (blockIdx.x * kUnits + u) / (2 * (uint32_t)c.Hkv);
+                if (j >= first && j >= end - pages && j < end) { at[u][0] = mine; at[u][1] = (int)(j - (end - pages)); }
+            }
+            if (threadIdx.x == kBlock - 1) behind = end;
+            __syncthreads();
+            before = behind;
+            __syncthreads();
+        }
+        __syncthreads();
+        if (unit >= a.units || at[unit_in_block][0] < 0) return;
+        b = at[unit_in_block][0];
+        slot = at[unit_in_block][1];
+    } else {
+        if (unit >= a.units) return;
+        b = (int)((nth >> 1) / (uint32_t)a.slots);
+        slot = (int)((nth >> 1) - (uint32_t)b * a.slots);
+    }
     Seq s;
     uint32_t bad = 0;
-    bool ok = load_seq(a.cu, a.kv_len, b, a.T, &s, &bad);
-    if (ok && s.len == 0) return;                             // padding
-    if (ok && s.n > a.max_new) { ok = false; bad = kBadRows; }
-    if (ok && s.len < s.n) { ok = false; bad = kBadLen; }
-    if (!ok) {
-        if (tid == 0 && slot == 0 && h == 0 && !values) latch(c, bad);
+    if (!append_seq(a, b, &s, &bad)) {
+        if (bad && tid == 0 && slot == 0 && h == 0 && !values) latch(c, bad);
         return;
     }
     const int start = s.len - s.n, p = (start >> c.page_log2) + slot;
@@ -221,7 +265,10 @@ template <typename T, int D, int CODE, int UT>
 cudaError_t run(AppendArgs a, cudaStream_t st) {
     constexpr int kBlock = block_threads(UT);
     const long long per = kBlock / UT;
-    const long long units = 2ll * a.c.B * a.slots * a.c.Hkv, kv_blocks = (units + per - 1) / per;
+    // Every sequence may have `slots` pages; all together touch at most T / page + 2 B.
+    const long long every = (long long)a.c.B * a.slots, touched = (long long)(a.T >> a.c.page_log2) + 2ll * a.c.B;
+    a.compact = every > 4 * touched;
+    const long long units = 2 * (a.compact ? touched : every) * a.c.Hkv, kv_blocks = (units + per - 1) / per;
     long long q_blocks = 0;
     if (a.q.p != nullptr) {
         const int heads = a.c.Hkv * a.c.G;

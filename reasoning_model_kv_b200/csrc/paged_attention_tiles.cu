@@ -390,9 +390,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     const float v = fmaxf(vs0, 7.9e-31f);        // 2^-100: its codes count for nothing
                     cc0 = id0 >= 0 ? ChunkConst{ks0 * sl, log2f(v), 1.f / v, 0.f} : ChunkConst{0.f, -INFINITY, 0.f, 0.f};
                 };
-                int idk[2] = {__shfl_sync(kFull, id0, 0), __shfl_sync(kFull, id0, 1)};
+                // a page's two groups of keys; values whose scale is zero are zeros
+                int idk[2], idv[2];
+                auto ids = [&](int i) {
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch) {
+                        idk[ch] = __shfl_sync(kFull, id0, 2 * (i & 15) + ch);
+                        idv[ch] = __shfl_sync(kFull, vs0 > 0.f ? id0 : -1, 2 * (i & 15) + ch);
+                    }
+                };
+                ids(0);
                 load(c.k_pool, 0, idk, kr);
-                load(c.v_pool, 0, idk, vr);
+                load(c.v_pool, 0, idv, vr);
                 constants();
                 // keys run one unit ahead of values: unit i's products wait for its keys first
                 auto put_keys = [&](int i) {
@@ -410,14 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             fetch(i + 17, id1, ks1, vs1);
                             constants();
                         }
-                        idk[0] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15));
-                        idk[1] = __shfl_sync(kFull, id0, 2 * ((i + 1) & 15) + 1);
+                        ids(i + 1);
                         load(c.k_pool, i + 1, idk, kr);
                     }
                 };
                 put_keys(0);
                 for (int i = 0; i < nu && ok; ++i) {
-                    const int idn[2] = {idk[0], idk[1]};                 // of unit i + 1
+                    const int idn[2] = {idv[0], idv[1]};                 // of unit i + 1
                     if (i + 1 < nu) put_keys(i + 1);
                     const uint32_t n = n_tile + i, st = n & 1;
                     if (n >= 2) ok = warp_wait(&bar.v_free[st], ((n >> 1) - 1) & 1) && ok;

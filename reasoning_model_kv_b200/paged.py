@@ -4,7 +4,7 @@ the current stream of the tensors' device."""
 from __future__ import annotations
 
 import ctypes
-from struct import Struct
+from struct import Struct, error as StructError
 
 import torch
 
@@ -48,6 +48,13 @@ def _run(index: int, fn, *args):
             status = fn(*args)
     if status:
         _check(status)
+
+
+def _pack(struct: Struct, *values) -> bytes:
+    try:
+        return struct.pack(*values)
+    except StructError as e:
+        _bad(f"argument out of range or not a number: {e}")
 
 
 def _rows(t: torch.Tensor, heads: int, dim: int, dtype, index: int, name: str):
@@ -140,7 +147,7 @@ def tkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: 
     p, r = _ints(pos, (T,), index, "pos"), rope._match(dtype, D, index)
     q_out, qo = _output(q_out, q, stream, "q_out")
     k_out, ko = _output(k_out, k, stream, "k_out")
-    args = _NORM_ROPE_ARGS.pack(*qr, *kr, *qo, *ko, p, r, T, Hq, Hkv, D, DTYPES[dtype])
+    args = _pack(_NORM_ROPE_ARGS, *qr, *kr, *qo, *ko, p, r, T, Hq, Hkv, D, DTYPES[dtype])
     _run(index, lib().tkv_qk_norm_rope, args, _current_stream(index) if stream is None else stream.cuda_stream)
     return q_out, k_out
 
@@ -148,10 +155,12 @@ def tkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: 
 class TkvPagedCache:
     """One layer's paged 8-bit cache: pools of pages with a scale for each (page, kv head),
     the append that fills them and the attention over them.  `pools` gives existing
-    (k_pool, v_pool, k_scale, v_scale) tensors, else they are made, zeroed."""
+    (k_pool, v_pool, k_scale, v_scale) tensors, else they are made, zeroed.  `share` is a cache
+    whose workspace (up to 40 MB) this one uses too: the layers of a model, say, whose calls
+    follow one another on one stream."""
 
     def __init__(self, B, Hkv, G, D, page, pages, max_pages, code="e4m3", dtype=torch.bfloat16, pools=None,
-                 device="cuda"):
+                 device="cuda", share: TkvPagedCache | None = None):
         if code not in CODES:
             _bad(f"code must be one of {sorted(CODES)}")
         if dtype not in DTYPES:
@@ -175,7 +184,12 @@ class TkvPagedCache:
                                   (self.v_scale, torch.float32, shape[:2], "v_scale")):
             if not t.is_cuda or t.device != self.device or t.dtype is not want or t.shape != sh or not t.is_contiguous():
                 _bad(f"{name} must be a contiguous {want} CUDA tensor {sh} on the pools' device")
-        self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+        if share is None:
+            self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+        else:
+            if share.device != self.device or share.workspace.numel() < nbytes + 256:
+                _bad("the shared workspace is on another device or too small")
+            self.workspace = share.workspace
         base = self.workspace.data_ptr()
         h = ctypes.c_void_p()
         _check(lib().tkv_paged_create(ctypes.byref(self.cfg), self.k_pool.data_ptr(), self.v_pool.data_ptr(),
@@ -184,8 +198,9 @@ class TkvPagedCache:
         self._h = h.value
         self._table_shape, self._len_shape, self._cu_shape = (B, max_pages), (B,), (B + 1,)
         self._append, self._attention = lib().tkv_paged_append, lib().tkv_paged_attention
-        self.reset()
-        torch.cuda.current_stream(self.device).synchronize()    # ready for any stream
+        if share is None:
+            self.reset()
+            torch.cuda.current_stream(self.device).synchronize()    # ready for any stream
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -221,7 +236,7 @@ class TkvPagedCache:
             q_out, qo = _output(q_out, q, stream, "q_out")
         elif q_out is not None:
             _bad("q_out without q")
-        _run(index, self._append, self._h, _APPEND_ARGS.pack(*kr, *vr, *qr, *qo, *lengths, r, T, max_new),
+        _run(index, self._append, self._h, _pack(_APPEND_ARGS, *kr, *vr, *qr, *qo, *lengths, r, T, max_new),
              _current_stream(index) if stream is None else stream.cuda_stream)
         return q_out
 
@@ -236,7 +251,7 @@ class TkvPagedCache:
         T = q.shape[0]
         lengths = self._lengths(block_table, kv_len, cu, T)
         out, o = _output(out, q, stream, "out")
-        _run(index, self._attention, self._h, _ATTENTION_ARGS.pack(*qr, *o, *lengths, T, max_q, window, softmax_scale),
+        _run(index, self._attention, self._h, _pack(_ATTENTION_ARGS, *qr, *o, *lengths, T, max_q, window, softmax_scale),
              _current_stream(index) if stream is None else stream.cuda_stream)
         return out
 

@@ -75,9 +75,8 @@ def attention(q, k_pool, v_pool, k_scale, v_scale, table, lens, cu, scale, windo
         n, L = cu[b + 1] - cu[b], max(0, lens[b])
         if n <= 0:
             continue
-        ids = [int(i) for i in table[b][:(L + page - 1) // page]]
-        live = torch.tensor([0 <= ids[j // page] < k_pool.shape[0] if j // page < len(ids) else False
-                             for j in range(L)], dtype=torch.bool)
+        ids = [int(table[b][i]) if i < len(table[b]) else -1 for i in range((L + page - 1) // page)]
+        live = torch.tensor([0 <= ids[j // page] < k_pool.shape[0] for j in range(L)], dtype=torch.bool)
         safe = torch.tensor([i if 0 <= i < k_pool.shape[0] else 0 for i in ids], dtype=torch.long)
         rows = slice(cu[b], cu[b + 1])
         at = torch.arange(L - n, L)

@@ -453,3 +453,133 @@ def test_binding_refuses_wrong_tensors():
             f()
             raise AssertionError(i)
     assert c.launch_count() == 0 and c.poll_error() == tkv.TKV_OK
+
+
+# ------------------------------------------------------------------ the rarer calls
+def test_append_one_long_sequence_among_many_short_ones():
+    """Far fewer pages than sequences times the longest one's: pages are numbered over the sequences."""
+    lens = [1 + (7 * i) % 40 for i in range(300)]
+    new = [1] * 300
+    lens[211], new[211] = 1000, 700
+    lens[17], new[17], lens[255], new[255], lens[256], new[256] = 0, 0, 40, 40, 30, 0
+    _check_append("e4m3", 16, lens, new, d=64, hkv=2, g=1)
+    _check_append("int8", 128, lens, new, d=128, hkv=3, g=1, with_q=False)
+
+
+def test_attention_of_many_sequences():
+    lens = [1 + (13 * i) % 70 for i in range(300)]
+    _attend(lens, [1] * 300, d=64, hkv=2, g=2)
+    lens = [3 + (11 * i) % 90 for i in range(600)]
+    _attend(lens, [3] * 600, d=64, hkv=1, g=16)
+
+
+def test_lengths_beyond_the_table_and_bad_rows():
+    gen = _gen(4)
+    page, hkv, g, d, B = 16, 1, 4, 64, 3
+    kp, ks = po.make_pool(gen, 8, hkv, page, d, "int8")
+    c = TkvPagedCache(B, hkv, g, d, page, 8, 2, code="int8", pools=(kp.cuda(), kp.cuda(), ks.cuda(), ks.cuda()))
+    table = _i32([[0, 1], [2, 3], [4, 5]])
+    nums = kp.float().double()
+    for nq in ([1, 1, 1], [20, 16, 15]):
+        q = torch.randn((sum(nq), g * hkv, d), generator=gen).to(BF16)
+        cu = _cu(nq)
+        run = lambda lens, cu=cu: c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), 0.1, cu=_i32(cu).cuda(), max_q=max(nq),
+                                              out=torch.full_like(q, 9.0).cuda()).cpu()
+        out = run([100, 32, 20])                                  # 100 tokens, room for 32
+        assert c.poll_error() == tkv.TKV_ERR_CAPACITY
+        want, tol = po.attention(q, nums, nums, ks, ks, table, [100, 32, 20], cu, 0.1, 0, page)
+        assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + tol).all()
+        out = run([-3, 32, 2 ** 31 - 1])                          # lengths that cannot be: zeros
+        assert c.poll_error() == tkv.TKV_ERR_INVALID
+        assert (out[:cu[1]] == 0).all() and (out[cu[2]:] == 0).all()
+        assert ((out[cu[1]:cu[2]].double() - want[cu[1]:cu[2]]).abs() <= (want.abs() * 2.0 ** -8 + tol)[cu[1]:cu[2]]).all()
+        for bad in ([0, -1, cu[2], cu[3]], [0, cu[1], cu[2], cu[3] + 1], [5 * cu[3], cu[1], cu[2], cu[3]]):
+            out = run([20, 32, 20], bad)
+            assert c.poll_error() == tkv.TKV_ERR_INVALID and not out.isnan().any()
+    k = torch.randn((5, hkv, d), generator=gen).to(BF16).cuda()
+    before = c.k_pool.clone()
+    for lens, cu in (([-1, 0, 0], [0, 1, 1, 1]), ([9, 9, 9], [0, 6, 6, 6]), ([9, 9, 9], [3, 1, 1, 1]), ([2 ** 31 - 1, 0, 0], [0, 1, 1, 1])):
+        c.append(k, k, table.cuda(), _i32(lens).cuda(), cu=_i32(cu).cuda(), max_new=5)
+        assert c.poll_error() == tkv.TKV_ERR_INVALID and torch.equal(c.k_pool, before)
+
+
+@pytest.mark.parametrize("nq", [[1, 1], [60, 40]])
+@pytest.mark.parametrize("page", [16, 64])
+def test_scales_of_zero_and_softmax_scales_of_either_sign(nq, page):
+    gen = _gen(6)
+    hkv, g, d, lens = 2, 4, 64, [200, 70]
+    table, pages = po.make_table(gen, lens, page, 14)
+    kp, ks = po.make_pool(gen, pages, hkv, page, d, "e4m3")
+    vp, vs = po.make_pool(gen, pages, hkv, page, d, "e4m3")
+    ks[int(table[0, 0])] = 0.0                  # keys of zeros in a page, values of zeros in another
+    vs[int(table[0, 1])] = 0.0
+    vs[int(table[1, 0])] = 0.0
+    for all_zero in (False, True):
+        if all_zero:
+            vs.zero_()
+        c = TkvPagedCache(2, hkv, g, d, page, pages, 14, pools=tuple(t.cuda() for t in (kp, vp, ks, vs)))
+        q = torch.randn((sum(nq), hkv * g, d), generator=gen).to(BF16)
+        cu = _cu(nq)
+        for scale in (0.125, -0.125, 0.0):
+            out = c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), scale, cu=_i32(cu).cuda(), max_q=max(nq)).cpu()
+            want, tol = po.attention(q, kp.float().double(), vp.float().double(), ks, vs, table, lens, cu, scale, 0, page)
+            assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + tol + 1e-38).all()
+            assert not all_zero or (out == 0).all()
+
+
+@pytest.mark.parametrize("nq", [[1, 1], [60, 40]])
+def test_output_over_the_queries_and_strided_rows(nq):
+    """The output may take the queries' place; rows may lie in a larger array, heads before tokens."""
+    gen = _gen(7)
+    page, hkv, g, d, lens = 32, 2, 4, 128, [3000, 500]
+    table, pages = po.make_table(gen, lens, page, 100)
+    kp, ks = po.make_pool(gen, pages, hkv, page, d, "int8")
+    c = TkvPagedCache(2, hkv, g, d, page, pages, 100, code="int8", dtype=FP16, pools=tuple(t.cuda() for t in (kp, kp, ks, ks)))
+    x = torch.randn((hkv * g, sum(nq), d + 4), generator=gen).to(FP16).cuda()
+    q = x[:, :, 4:].transpose(0, 1)
+    args = (table.cuda(), _i32(lens).cuda(), 0.08)
+    kw = dict(cu=_i32(_cu(nq)).cuda(), max_q=max(nq))
+    want = c.attention(q.contiguous(), *args, **kw)
+    assert torch.equal(c.attention(q, *args, **kw), want)
+    assert c.attention(q, *args, out=q, **kw) is q and torch.equal(q, want)
+    assert c.poll_error() == tkv.TKV_OK
+
+
+def test_layers_share_a_workspace():
+    gen = _gen(12)
+    page, hkv, g, d, B = 64, 2, 8, 128, 2
+    a = TkvPagedCache(B, hkv, g, d, page, 40, 20)
+    b = TkvPagedCache(B, hkv, g, d, page, 40, 20, code="int8", share=a)
+    small = TkvPagedCache(1, 1, 1, 64, 16, 1, 1)
+    assert b.workspace is a.workspace
+    with pytest.raises(TkvError):
+        TkvPagedCache(B, hkv, g, d, page, 40, 20, share=small)
+    alone = TkvPagedCache(B, hkv, g, d, page, 40, 20, code="int8", pools=(b.k_pool, b.v_pool, b.k_scale, b.v_scale))
+    table = torch.randperm(40, generator=gen).to(torch.int32).view(B, 20).cuda()
+    lens, cu = _i32([1280, 900]).cuda(), _i32([0, 1280, 2180]).cuda()
+    x = torch.randn((2180, hkv, d), generator=gen).to(BF16).cuda()
+    for c in (a, b):
+        c.append(x, x, table, lens, cu=cu, max_new=1280)
+    for _ in range(3):
+        for rows in (2, 100):
+            q = torch.randn((rows, hkv * g, d), generator=gen).to(BF16).cuda()
+            kw = dict(cu=_i32([0, rows // 2, rows]).cuda(), max_q=rows // 2)
+            oa, ob = a.attention(q, table, lens, 0.1, **kw), b.attention(q, table, lens, 0.1, **kw)
+            assert torch.equal(ob, alone.attention(q, table, lens, 0.1, **kw))
+            # the same keys and values, in other codes: E4M3 is off by 2^-4 of a value at most
+            assert (oa.float() - ob.float()).abs().max() < 0.5
+    assert a.poll_error() == tkv.TKV_OK
+
+
+def test_arguments_that_no_struct_holds():
+    c = TkvPagedCache(1, 1, 1, 64, 16, 1, 1)
+    q = torch.zeros((1, 1, 64), dtype=BF16, device="cuda")
+    t, n = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for kw in (dict(window=1 << 40), dict(max_q=2.5), dict(window=None)):
+        with pytest.raises(TkvError):
+            c.attention(q, t, n, 0.1, **kw)
+    with pytest.raises(TkvError):
+        c.attention(q, t, n, "no")
+    with pytest.raises(TkvError):
+        c.append(q, q, t, n, max_new=1 << 33)
+    assert c.launch_count() == 0
