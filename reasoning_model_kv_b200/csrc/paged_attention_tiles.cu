@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     const uint32_t base = sub ? n_tile1 : n_tile;       // tiles of this half before the item
                     for (int i = 0; i < nu && ok; ++i) {
                         const uint32_t n = base + i, kt = n_tile + i;
-                        ok = warp_wait(&bar.c_full[kt & (kConstSets - 1)], (kt / kConstSets) & 1);
+                        // An item without a second tile of rows is passed over by that tile's warps, and
+                        // the codes' phases they have not followed are met again with S.
+                        if (i == 0) ok = warp_wait(&bar.s_full[sub], n & 1);
+                        ok = ok && warp_wait(&bar.c_full[kt & (kConstSets - 1)], (kt / kConstSets) & 1);
                         // read while S is formed: with eight reads behind it a unit took an eighth longer
                         const ChunkConst *cc = consts[kt & (kConstSets - 1)];
                         constexpr int kKeys = kUnit / SETS;

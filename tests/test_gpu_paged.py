@@ -262,6 +262,13 @@ def test_attention_whole_prompts(page):
     _attend([257, 128, 1, 390], [257, 128, 1, 390], page=page, g=2, hkv=2)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+def test_attention_items_of_one_and_two_row_tiles_in_turn(page):
+    """A block that goes from an item with few rows (half of a block's softmax warps have none)
+    to one with many, over sequences of several units: scales differ from page to page."""
+    _attend([1000 + 17 * i for i in range(24)], [90] * 24, page=page, hkv=4, g=4, scales=(-9, -3))
+
+
 def test_attention_rows_of_no_sequence_and_negative_positions():
     _attend([40, 70], [3, 2], first=2, behind=5)
     _attend([2, 0, 30], [5, 3, 1])                      # rows before a sequence's first token: zeros
