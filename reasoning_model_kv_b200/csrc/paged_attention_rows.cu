@@ -401,15 +401,20 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-                float *const wt = reinterpret_cast<float *>(ring_all);   // [part][row] weights
-                for (int i = tid; i < parts * kRows; i += kThreads) wt[i] = __ldcg(slot_of(cut.first + i / kRows) + i % kRows);
+                float *const wt = reinterpret_cast<float *>(ring_all);   // [part][row] maxima, then weights
+                float *const zt = wt + kOwnParts * kRows;                // sums
+                for (int i = tid; i < parts * kRows; i += kThreads) {
+                    const float *p = slot_of(cut.first + i / kRows) + i % kRows;
+                    wt[i] = __ldcg(p);
+                    zt[i] = __ldcg(p + kRows);
+                }
                 __syncthreads();
                 if (tid < kRows) {
                     float n = attn::kNoMax, zz = 0.f;
                     for (int i = 0; i < parts; ++i) n = fmaxf(n, wt[i * kRows + tid]);
                     for (int i = 0; i < parts; ++i) {
                         const float w = ex2(wt[i * kRows + tid] - n);
-                        zz = fmaf(__ldcg(slot_of(cut.first + i) + kRows + tid), w, zz);
+                        zz = fmaf(zt[i * kRows + tid], w, zz);
                         wt[i * kRows + tid] = w;
                     }
                     sm_z[0][tid] = zz > 0.f || zz != zz ? 1.f / zz : 0.f;

@@ -30,6 +30,7 @@ _NORM_ROPE_ARGS = Struct("@PqqPqqPqqPqqPPiiiii4x")
 _APPEND_ARGS = Struct("@PqqPqqPqqPqqPPPPii")
 _ATTENTION_ARGS = Struct("@PqqPqqPPPiiif")
 _NO_ROWS = (0, 0, 0)
+_CONTIGUOUS = torch.contiguous_format
 
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
@@ -59,30 +60,25 @@ def _pack(struct: Struct, *values) -> bytes:
 
 def _rows(t: torch.Tensor, heads: int, dim: int, dtype, index: int, name: str):
     """(address, token stride, head stride) of a [T, heads, dim] tensor."""
-    st = t.stride()
-    if len(st) != 3 or t.shape[1:] != (heads, dim):
-        _bad(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        _bad(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        _bad(f"{name} must be on cuda:{index}, got {t.device}")
-    if st[2] != 1:
+    shape = t.shape
+    if len(shape) == 3 and shape[1] == heads and shape[2] == dim and t.dtype is dtype and t.get_device() == index:
+        st = t.stride()
+        if st[2] == 1:
+            return t.data_ptr(), st[0], st[1]
         _bad(f"{name} must have a contiguous head dim")
-    return t.data_ptr(), st[0], st[1]
+    _bad(f"{name} must be {dtype} [T, {heads}, {dim}] on cuda:{index}, got {t.dtype} {tuple(shape)} on {t.device}")
 
 
 def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        _bad(f"{name} must be contiguous int32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != index:
-        _bad(f"{name} must be on cuda:{index}, got {t.device}")
-    return t.data_ptr()
+    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _bad(f"{name} must be contiguous int32 {tuple(shape)} on cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _output(out, like: torch.Tensor, stream, name: str):
     """(out, its address and strides): a new contiguous tensor of the rows' shape, or `out`."""
     if out is None:
-        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+        out = torch.empty_like(like, memory_format=_CONTIGUOUS)
         if stream is not None:
             out.record_stream(stream)
         _, heads, dim = like.shape
@@ -136,12 +132,14 @@ def tkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: 
     """Norm and rotation of q [T, Hq, D] and k [T, Hkv, D] (bf16 or fp16, any token and head
     strides that are multiples of 4) at positions pos [T] int32; returns (q', k').  The outputs
     may be the inputs."""
-    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
+    q_shape, k_shape, dtype, index = q.shape, k.shape, q.dtype, q.get_device()
+    if len(q_shape) != 3 or len(k_shape) != 3 or index < 0:
         _bad("q and k must be CUDA tensors [T, heads, D]")
-    (T, Hq, D), Hkv, dtype, index = q.shape, k.shape[1], q.dtype, q.get_device()
+    T, Hq, D = q_shape
+    Hkv = k_shape[1]
     if dtype not in DTYPES:
         _bad(f"q must be bf16 or fp16, got {dtype}")
-    if k.shape[0] != T:
+    if k_shape[0] != T:
         _bad("q and k must have the same number of tokens")
     qr, kr = _rows(q, Hq, D, dtype, index, "q"), _rows(k, Hkv, D, dtype, index, "k")
     p, r = _ints(pos, (T,), index, "pos"), rope._match(dtype, D, index)
