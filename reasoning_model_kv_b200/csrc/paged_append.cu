@@ -5,6 +5,10 @@
 // magnitude, settle the scale, round what the page held before if the scale grew, and write
 // the codes.  So the rows are read once, a scale has one writer and nothing needs an atomic.
 // Units of small pages share a block.  The queries' rows are blocks of the same launch.
+// Measured: eight prompt chunks (21 thousand tokens, 475 MB) in 100 us = 4.7 TB/s, where the
+// queries' part streams and the units wait for memory and their barrier (the two kinds of
+// blocks in turn were no faster); one token of 64 sequences in 7.6 us, a chain of dependent
+// reads (lengths, page, scale and rows).
 #include <climits>
 
 #include <cuda_fp8.h>

@@ -12,6 +12,10 @@
 // to the largest scale so far (P in fp16 times 2^7: weights down to 2^-31 of the largest
 // count; they are rounded to 11 bits, more than either output type keeps).
 // The maximum moves only when a logit passes it by 2^8, so most tiles rescale nothing.
+// Measured: 64 sequences of 32k E4M3 tokens, 4.30 GB, in 665 us = 6.46 TB/s (copy rate 6.55); one
+// sequence of 131k int8 tokens, 269 MB, in 56 us = 4.8 TB/s (the split's ends and the join); 3 to
+// 6 rows of 16 sequences with four heads a kv head (24 rows), 194 MB, in 72 us = 2.7 TB/s: eight
+// warps of 255 registers an SM leave the latency of their instructions uncovered.
 #include <type_traits>
 
 #include "norm_rope.cuh"

@@ -13,6 +13,13 @@
 // carries the value scale, O = sum P code, and the softmax sum is sum P / value scale, so both
 // have one running maximum M, which moves only when y passes it by 2^8.  P is fp16 times 2^7
 // (11 bits, more than either output type keeps; down to 2^-31 of the largest).
+//
+// Measured: two chunks of 2048 rows x 32 heads on 14k and 16k keys, 961 GFLOP, in 925 us = 1.04
+// PFLOP/s, 63 % of the library's bf16 product.  Tensor cores and exponentials are each busy 46 %
+// of the time: a unit's softmax follows its S and precedes its O, and the second tile of rows
+// covers only part of that.  Slower: two threads a row (16 softmax warps), the maximum and P in
+// one pass with a second one where the maximum moved, an issuing warp for each tile of rows (its
+// products take turns with the other's; 312 -> 380 us on 2048 rows x 16 heads x 8k keys).
 #include <cuda_fp8.h>
 
 #include "f32x2.cuh"
