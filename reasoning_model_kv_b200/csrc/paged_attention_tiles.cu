@@ -124,19 +124,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const long long end = min(begin + share, plan.total);
     bool ok = true;
     if (begin >= plan.total) {
-        if (tid == 0 && a.cut) a.cut[blockIdx.x].parts = 0;
+        if (tid == 0) a.cut[blockIdx.x].parts = 0;
     } else {
         Cursor k;
         cursor_start(a, plan, begin, kUnitLog2, &k);
         uint32_t n_tile = 0, n_item = 0;          // units and items behind
         uint32_t n_tile1 = 0, n_item1 = 0;        // of the second tile of rows
         if (warp < 8) {
+            // 176, 104 and 56 registers for the three kinds of warps: the launch's 512 x 128 in all
             asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
             const int sub = warp >> 2, row = tid & 127;
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;
             const uint32_t s_col = tb + lanes + kColS + 128 * sub, o_col = tb + lanes + kColO + 128 * sub;
             const int ti = row / c.G, hd = row - ti * c.G;
-            if (tid == 0 && a.cut) a.cut[blockIdx.x].parts = 0;
+            if (tid == 0) a.cut[blockIdx.x].parts = 0;
             do {
                 int u0, nu;
                 cursor_units(k, begin, end, &u0, &nu);
@@ -342,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     const int u = i0 + (lane >> 1), t = t_item + (u << kUnitLog2) + 16 * (lane & 1);
                     id = -1;
                     ks = vs = 0.f;
-                    if (u < nu && t < k.r.hi && t + 15 >= k.r.lo) {
+                    // (constants read for 64 keys are those of their first 16, visible or not)
+                    if (u < nu && t < k.r.hi && (t | (kUnit / SETS - 1)) >= k.r.lo) {
                         uint32_t bad = 0;
                         id = load_page(c, a.block_table, k.b, t >> c.page_log2, &bad);
                         if (id >= 0) {

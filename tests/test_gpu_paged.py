@@ -269,6 +269,15 @@ def test_attention_items_of_one_and_two_row_tiles_in_turn(page):
     _attend([1000 + 17 * i for i in range(24)], [90] * 24, page=page, hkv=4, g=4, scales=(-9, -3))
 
 
+@pytest.mark.parametrize("code,dtype,d", [("e4m3", BF16, 128), ("int8", FP16, 64)])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("window", [1, 17, 100, 333])
+def test_attention_windows_that_begin_inside_a_page(code, dtype, d, page, window):
+    """Row tiles whose first visible key is anywhere in its page, for single rows and chunks."""
+    for nq in ([60, 45, 9], [1, 1, 1], [5, 3, 4]):
+        _attend([500, 313, 777], nq, page=page, d=d, hkv=1, g=4, code=code, dtype=dtype, window=window, scales=(-9, -3))
+
+
 def test_attention_rows_of_no_sequence_and_negative_positions():
     _attend([40, 70], [3, 2], first=2, behind=5)
     _attend([2, 0, 30], [5, 3, 1])                      # rows before a sequence's first token: zeros
