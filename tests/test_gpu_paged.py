@@ -599,3 +599,32 @@ def test_arguments_that_no_struct_holds():
     with pytest.raises(TkvError):
         c.append(q, q, t, n, max_new=1 << 33)
     assert c.launch_count() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 50])
+def test_queries_that_see_nothing_and_calls_without_rows(rows):
+    """NaN queries of padded sequences give zeros and reach nobody else; rows of no sequence at all
+    are a call that writes nothing, also as the first one in a captured graph."""
+    gen = _gen(14)
+    page, hkv, g, d = 64, 1, 8, 128
+    c = TkvPagedCache(3, hkv, g, d, page, 4, 4)
+    c.k_pool.copy_(torch.randn(c.k_pool.shape, generator=gen).cuda().mul_(50).to(torch.float8_e4m3fn))
+    c.v_pool.copy_(c.k_pool.flip(0))
+    c.k_scale.fill_(2.0 ** -6), c.v_scale.fill_(2.0 ** -6)
+    table = _i32([[0, 1, 2, 3]] * 3).cuda()
+    q = torch.randn((3 * rows, hkv * g, d), generator=gen).to(BF16).cuda()
+    want = c.attention(q, table, _i32([0, 200, 0]).cuda(), 0.1, cu=_i32([0, rows, 2 * rows, 3 * rows]).cuda(), max_q=rows)
+    q[:rows] = math.nan
+    q[2 * rows:] = math.inf
+    got = c.attention(q, table, _i32([0, 200, 0]).cuda(), 0.1, cu=_i32([0, rows, 2 * rows, 3 * rows]).cuda(), max_q=rows)
+    assert torch.equal(got, want) and (got[:rows] == 0).all() and (got[2 * rows:] == 0).all()
+    fresh = TkvPagedCache(3, hkv, g, d, page, 4, 4, code="int8", dtype=FP16)
+    out = torch.full((3 * rows, hkv * g, d), 5.0, dtype=FP16, device="cuda")
+    cu, lens, qh = _i32([0, 0, 0, 0]).cuda(), _i32([9, 9, 9]).cuda(), q.half()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        fresh.attention(qh, table, lens, 0.1, cu=cu, max_q=rows, out=out)
+        fresh.append(qh[:, :1], qh[:, :1], table, lens, cu=cu, max_new=rows)
+    gr.replay()
+    gr.replay()
+    assert (out == 5.0).all() and (fresh.k_pool == 0).all() and fresh.poll_error() == tkv.TKV_OK
