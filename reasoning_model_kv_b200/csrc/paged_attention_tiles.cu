@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         uint32_t s[128];
 #pragma unroll
                         for (int j = 0; j < 128; j += 32) tc::ld32(s_col + j, s + j);
-                        tc::wait_ld();
+                        tc::wait_ld<128>(s);
                         const int t0 = (k.r.tile0 + u0 + i) << kUnitLog2;
                         if (t0 + kUnit - 1 > sub_first || (a.window && t0 <= sub_last - a.window)) {
                             const int hi = pos - t0, lo = a.window ? hi - a.window : -1;      // lo < key <= hi
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                                 for (int j = 0; j < D; j += 16) {
                                     uint32_t o[16];
                                     tc::ld16(o_col + j, o);
-                                    tc::wait_ld();
+                                    tc::wait_ld<16>(o);
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
                                     tc::st16(o_col + j, o);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         for (int j = 0; j < D; j += 16) {
                             uint32_t o[16];
                             tc::ld16(o_col + j, o);
-                            tc::wait_ld();
+                            tc::wait_ld<16>(o);
                             if (live && ok) {
 #pragma unroll
                                 for (int e = 0; e < 16; e += 4)
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         for (int j = 0; j < D; j += 16) {
                             uint32_t o[16];
                             tc::ld16(o_col + j, o);
-                            tc::wait_ld();
+                            tc::wait_ld<16>(o);
                             if (live) {
 #pragma unroll
                                 for (int e = 0; e < 16; e += 4)
