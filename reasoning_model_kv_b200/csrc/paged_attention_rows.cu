@@ -458,8 +458,8 @@ cudaError_t run(AttnArgs a, cudaStream_t st, int64_t *launches) {
     kernel<<<blocks, kThreads, smem_bytes<D, NT>(), st>>>(a);
     e = cudaGetLastError();
     ++*launches;
-    // no item has more units than the block table has room for
-    if (e == cudaSuccess && (((long long)a.c.max_pages * a.c.page + kUnit - 1) >> kUnitLog2) + 1 > kOwnParts) {
+    // no item has more units than the block table has room for (key_range)
+    if (e == cudaSuccess && ((a.room + kUnit - 1) >> kUnitLog2) + 1 > kOwnParts) {
         e = launch_join(a, blocks, 8 * NT, 8 * NT, st);
         ++*launches;
     }

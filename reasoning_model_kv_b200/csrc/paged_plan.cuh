@@ -26,6 +26,7 @@ struct AttnArgs {
     Rows q, out;
     const int32_t *block_table, *kv_len, *cu;
     int T, window;
+    int room;               // tokens that a row of the block table has pages for
     float scale_log2;       // softmax_scale * log2(e)
     int tile_tokens;        // query tokens of an item
     int item_cost;          // an item's setup in units
@@ -35,7 +36,9 @@ struct AttnArgs {
     CutItem *cut;           // [blocks]
 };
 
-// Key range of query tokens [i0, i1) of a sequence, and its tiles of `unit` keys.
+// Key range of query tokens [i0, i1) of a sequence, and its tiles of `unit` keys.  It ends with
+// the block table: a length beyond it (the plan latches it) adds no units, so an item has no more
+// of them than the table has room for.
 struct KeyRange {
     int first, lo, hi;      // position of token i0; keys [lo, hi) are seen by some row
     int tile0, units;       // units >= 1
@@ -44,7 +47,7 @@ __device__ __forceinline__ KeyRange key_range(const AttnArgs &a, const Seq &s, i
     KeyRange r;
     const int i1 = min(i0 + a.tile_tokens, s.n);
     r.first = s.len - s.n + i0;
-    r.hi = max(0, s.len - s.n + i1);
+    r.hi = min(max(0, s.len - s.n + i1), a.room);
     r.lo = a.window ? max(0, r.first - a.window + 1) : 0;
     r.tile0 = r.lo >> unit_log2;
     r.units = max(1, ((r.hi + (1 << unit_log2) - 1) >> unit_log2) - r.tile0);
@@ -100,7 +103,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warp_sum
 }
 
 // Finds the block's stretch: *share places from *begin on (none if begin >= total), and where
-// that is.  Block 0 reports sequences that cannot be used.  All NT threads take part.
+// that is.  Block 0 reports sequences that cannot be used, or whose last token (which their last
+// row sees) the block table has no room for.  All NT threads take part.
 template <int NT>
 __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_log2, long long *begin, long long *share) {
     const int B = a.c.B, tid = threadIdx.x;
@@ -108,6 +112,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_l
     for (int b = tid; b < B; b += NT) {
         uint32_t bad;
         const Seq s = attention_seq(a, b, &bad);
+        if (!bad && s.n > 0 && s.len > a.room) bad = kNoPage;
         if (bad && blockIdx.x == 0) latch(a.c, bad);
         mine = head_units(a, s, unit_log2) * a.c.Hkv;
         sum += mine;
