@@ -459,7 +459,7 @@ typedef struct {
     tkv_rows q, q_out;             /* [T][Hkv*G][D], or both NULL                */
     const int32_t *block_table, *kv_len, *cu;
     const tkv_rope *rope;          /* or NULL                                    */
-    int32_t T;
+    int32_t T;                     /* rows (0 .. 2^30)                           */
     int32_t max_new;               /* bound on a sequence's new tokens (1 .. 2^30) */
 } tkv_paged_append_args;
 
@@ -479,10 +479,10 @@ TKV_API tkv_status tkv_paged_append(tkv_paged *cache, const tkv_paged_append_arg
 typedef struct {
     tkv_rows q, out;               /* [T][Hkv*G][D]                              */
     const int32_t *block_table, *kv_len, *cu;
-    int32_t T;
+    int32_t T;                     /* rows (0 .. 2^30)                           */
     int32_t max_q;                 /* bound on a sequence's query rows (>= 1); it only
                                       chooses the kernel                          */
-    int32_t window;                /* >= 0                                       */
+    int32_t window;                /* >= 0; from 2^30 on as 0: every key         */
     float softmax_scale;           /* finite                                     */
 } tkv_paged_attention_args;
 

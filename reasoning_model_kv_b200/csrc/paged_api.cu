@@ -78,7 +78,7 @@ tkv_status bad(const char *why) { return api_fail(TKV_ERR_INVALID, why); }
 const char *lengths_fault(const tkv_paged *c, const int32_t *table, const int32_t *len, const int32_t *cu, int T) {
     if (!table || !len) return "NULL block_table or kv_len";
     if (!aligned(table, 4) || !aligned(len, 4) || !aligned(cu, 4)) return "int32 arrays must be 4-byte aligned";
-    if (T < 0) return "T must be >= 0";
+    if (T < 0 || T > tkv::paged::kMaxLen) return "T must be in [0, 2^30]";
     if (!cu && T != c->cfg.B) return "without cu, T must be B";
     return nullptr;
 }

@@ -20,7 +20,10 @@ cudaError_t launch_attention(const View &c, Rows q, Rows out, int T, const int32
     AttnArgs a{};
     a.c = c; a.q = q; a.out = out;
     a.block_table = block_table; a.kv_len = kv_len; a.cu = cu;
-    a.T = T; a.window = window;
+    a.T = T;
+    // a window as long as the longest sequence hides nothing; positions less a shorter one stay
+    // within 32 bits
+    a.window = window >= kMaxLen ? 0 : window;
     a.room = c.max_pages * c.page;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.arrived = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(c.err) + 256);

@@ -108,3 +108,19 @@ def test_tokens_that_the_table_has_no_room_for_count_as_masked(length, nq, windo
                     out=out)
         assert c.poll_error() == tkv.TKV_ERR_CAPACITY
         check(out, *exact(q, pools, table, lens, rows, d ** -0.5, window, page, 448.0), BF16)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 30, 1 << 30, (1 << 30) - 1, 7])
+@pytest.mark.parametrize("lens,nq", [([2, 3], [5, 1]), ([2, 0], [4, 3]), ([20, 70], [45, 60]), ([3, 200], [90, 33])])
+def test_windows_without_an_end_and_rows_at_negative_positions(window, lens, nq):
+    gen = torch.Generator().manual_seed(sum(lens))
+    page, hkv, g, d, mp = 32, 2, 2, 128, 8
+    pools = _small_pools(gen, 16, hkv, page, d, "int8")
+    table = torch.randperm(16, generator=gen).to(torch.int32).view(2, mp)
+    c = TkvPagedCache(2, hkv, g, d, page, 16, mp, code="int8", dtype=FP16, pools=pools)
+    q = torch.randn((sum(nq), hkv * g, d), generator=gen).to(FP16)
+    out = torch.full_like(q, 9.0).cuda()
+    c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), d ** -0.5, cu=_i32(_cu(nq)).cuda(), max_q=max(nq), window=window,
+                out=out)
+    assert c.poll_error() == tkv.TKV_OK
+    check(out, *exact(q, pools, table, lens, nq, d ** -0.5, window, page, 127.0), FP16)

@@ -136,3 +136,13 @@ def test_oracle_scale_and_codes():
     out, _ = po.attention(q, k, v, one, one, [[0]], [2], [0, 1], 0.125, 0, 16)
     e = 2.718281828459045
     assert abs(out[0, 0, 0].item() - e / (1 + e)) < 1e-12
+
+
+def test_more_rows_than_positions_are_refused():
+    """T up to 2^30, so that a row's position less a window stays within 32 bits."""
+    L, h, p = tkv.lib(), _create(), 1 << 24
+    row = [p, 0, 128]
+    for T in ((1 << 30) + 1, (1 << 31) - 1):
+        assert L.tkv_paged_append(h, paged._APPEND_ARGS.pack(*row, *row, 0, 0, 0, 0, 0, 0, p, p, p, 0, T, 1), None) == INV
+        assert L.tkv_paged_attention(h, paged._ATTENTION_ARGS.pack(*row, p, 1024, 128, p, p, p, T, 1, 0, 0.1), None) == INV
+    assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_destroy(h) == 0
