@@ -8,9 +8,12 @@
 // in fp16: E4M3 through the hardware's conversion, integers as 0x6480 | code less 1152.  The
 // dims' order along QK's sum and the order of O's rows are free, so a lane takes 16-byte
 // chunks: of rows g and g + 8 of K, and of four tokens of V whose bytes it interleaves.
-// A page's key scale multiplies the fp32 products; its value scale is folded into P relative
-// to the largest scale so far (P in fp16 times 2^7: weights down to 2^-31 of the largest
-// count; they are rounded to 11 bits, more than either output type keeps).
+// A page's key scale multiplies the fp32 products of Q K, its value scale those of P V, which are
+// formed for 16 keys at a time: weights are relative to weights alone, whatever the scales are.
+// P is fp16 times 2^7: rounded to 11 bits, more than either output type keeps, and to multiples
+// of 2^-31 of the row's largest weight.  The second rounding matters where a value is far larger
+// than those that carry the weight, so keys whose scale is over 2^10 times the smallest one's are
+// multiplied in fp32 (kWide; four times the instructions).
 // The maximum moves only when a logit passes it by 2^8, so most tiles rescale nothing.
 // Measured: 64 sequences of 32k E4M3 tokens, 4.30 GB, in 665 us = 6.46 TB/s (copy rate 6.55); one
 // sequence of 131k int8 tokens, 269 MB, in 56 us = 4.8 TB/s (the split's ends and the join); 3 to
@@ -36,6 +39,9 @@ constexpr int kThreads = 128, kWarps = 4, kUnitLog2 = 6, kUnit = 64;
 constexpr int kStages = 4;
 // An item's setup takes about as long as this many units.
 constexpr int kItemCost = 4;
+constexpr float kWide = 1024.f;
+// Sums of weights times values: 2^15 above them is room for weights of 2^8 times 2^7.
+constexpr float kSumUnit = 1.f / 32768.f;
 // Parts that the last block to arrive joins by itself; more are left to the join kernel, whose
 // rows are spread over the card (one block joined 56 parts of 8 rows in 14 us, it in 3).
 constexpr int kOwnParts = 16;
@@ -72,8 +78,50 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 struct Stage {
     float ks, vs;      // the page's scales
     int live;          // 0: no page to read
-    int pad;
+    int wide;          // the products with its values are formed in fp32
 };
+
+// o += P V of 16 keys in fp32: the lane's rows 2 tig, 2 tig + 1 of every row tile and its D / 8 dims,
+// which are 16 (8) codes of every key.  p as the products S left it, f the values' factor.
+template <int D, int CODE, int NT>
+__device__ __forceinline__ void plain_values(uint32_t vt, float f, const float (&p)[NT][4], float (&o)[NT][D / 16][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            uint32_t w[D / 32];
+            if constexpr (D == 128) {
+                const uint4 u = lds128(vt + chunk_at<D>(j + 8 * half, g));
+                w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+            } else {
+                const uint2 u = lds64(vt + chunk_at<D>(j + 8 * half, g >> 1) + 8 * (g & 1));
+                w[0] = u.x; w[1] = u.y;
+            }
+            float pj[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) pj[nt][e] = __shfl_sync(kFull, p[nt][e + 2 * half], 4 * j + tig) * f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t c[2];
+                code_pairs<CODE>(w[i], c[0], c[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 v = __half22float2(attn::u32_as_h2(c[k]));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            o[nt][2 * i + k][e] = fmaf(pj[nt][e], v.x, o[nt][2 * i + k][e]);
+                            o[nt][2 * i + k][e + 2] = fmaf(pj[nt][e], v.y, o[nt][2 * i + k][e + 2]);
+                        }
+                }
+            }
+        }
+    }
+}
 
 template <int D, int NT>
 constexpr int ring_bytes() { return kWarps * kStages * 2 * 16 * D; }
@@ -132,12 +180,21 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
         };
         fetch(0, id0, ks0, vs0);
         fetch(32, id1, ks1, vs1);
+        // the smallest value scale but zero of the units so far, at first of the first 64
+        float low = INFINITY;
+        auto lower = [&](float vs) {
+            vs = vs > 0.f ? vs : INFINITY;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) vs = fminf(vs, __shfl_xor_sync(kFull, vs, s));
+            low = fminf(low, vs);
+        };
         // The copies of unit i's keys and values, and what its products need of the page.
         auto copy = [&](int i) {
             if (i < nu) {
                 if ((i & 31) == 0 && i > 0) {
                     id0 = id1; ks0 = ks1; vs0 = vs1;
                     fetch(i + 32, id1, ks1, vs1);
+                    lower(vs0);
                 }
                 const int id = __shfl_sync(kFull, id0, i & 31);
                 const int st = i % kStages, t = tok0 + (i << kUnitLog2);
@@ -167,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             if (i < nu) {
                 const int id = __shfl_sync(kFull, id0, i & 31);
                 const float ks = __shfl_sync(kFull, ks0, i & 31), vs = __shfl_sync(kFull, vs0, i & 31);
-                if (lane == 0) stage_info[warp][i % kStages] = Stage{ks, vs, id >= 0, 0};
+                if (lane == 0) stage_info[warp][i % kStages] = Stage{ks, vs, id >= 0, vs > low * kWide};
             }
         };
         // the first copies go out before the queries are read and before the scales are there
@@ -215,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             qinv[nt][0] = __shfl_sync(kFull, inv, 8 * tig);
             qinv[nt][1] = __shfl_sync(kFull, inv, 8 * tig + 4);
         }
-        float o[NT][kSteps][4], m[NT][2], z[NT][2], vref = 0.f;
+        float o[NT][kSteps][4], m[NT][2], z[NT][2];      // o: in units of kSumUnit
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = attn::kNoMax;
@@ -224,6 +281,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             for (int s = 0; s < kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
         }
         const int last_pos = k.r.first + tokens - 1;
+        lower(vs0);
+        lower(vs1);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) note(i);
         for (int i = 0; i < nu; ++i) {
@@ -285,50 +344,52 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                             for (int s = 0; s < kSteps; ++s) { o[nt][s][e] *= r; o[nt][s][e + 2] *= r; }
                         }
                 }
-                if (info.vs > vref) {
-                    const float r = vref / info.vs;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[nt][s][e] *= r;
-                    vref = info.vs;
-                }
-                const float pf = vref > 0.f ? info.vs / vref * 128.f : 0.f;
-                uint32_t pb[NT][2];
+                const float vs = info.vs * kSumUnit;
+                float p[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2(x[nt][e] - m[nt][e & 1]);
-                    z[nt][0] += p[0] + p[2];
-                    z[nt][1] += p[1] + p[3];
-                    pb[nt][0] = transpose8x8(attn::f32x2_to_f16x2(p[0] * pf, p[1] * pf));
-                    pb[nt][1] = transpose8x8(attn::f32x2_to_f16x2(p[2] * pf, p[3] * pf));
+                    for (int e = 0; e < 4; ++e) p[nt][e] = ex2(x[nt][e] - m[nt][e & 1]);
+                    z[nt][0] += p[nt][0] + p[nt][2];
+                    z[nt][1] += p[nt][1] + p[nt][3];
                 }
-                // V: words of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-                constexpr int kWords = D / 32;
-                uint32_t v[4][kWords];
+                if (info.wide) {
+                    plain_values<D, CODE, NT>(vt, vs * 128.f, p, o);
+                } else {
+                    uint32_t pb[NT][2];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 2 * tig + (r & 1) + 8 * (r >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 q4 = lds128(vt + chunk_at<D>(row, g));
-                        v[r][0] = q4.x; v[r][1] = q4.y; v[r][2] = q4.z; v[r][3] = q4.w;
-                    } else {
-                        const uint2 q2 = lds64(vt + chunk_at<D>(row, g >> 1) + 8 * (g & 1));
-                        v[r][0] = q2.x; v[r][1] = q2.y;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        pb[nt][0] = transpose8x8(attn::f32x2_to_f16x2(p[nt][0] * 128.f, p[nt][1] * 128.f));
+                        pb[nt][1] = transpose8x8(attn::f32x2_to_f16x2(p[nt][2] * 128.f, p[nt][3] * 128.f));
                     }
-                }
+                    // V: words of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+                    constexpr int kWords = D / 32;
+                    uint32_t v[4][kWords];
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const uint32_t sel = s & 1 ? 0x7362 : 0x5140;
-                    uint32_t a0, a1, a2, a3;
-                    code_pairs<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
-                    code_pairs<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 2 * tig + (r & 1) + 8 * (r >> 1);
+                        if constexpr (D == 128) {
+                            const uint4 q4 = lds128(vt + chunk_at<D>(row, g));
+                            v[r][0] = q4.x; v[r][1] = q4.y; v[r][2] = q4.z; v[r][3] = q4.w;
+                        } else {
+                            const uint2 q2 = lds64(vt + chunk_at<D>(row, g >> 1) + 8 * (g & 1));
+                            v[r][0] = q2.x; v[r][1] = q2.y;
+                        }
+                    }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][s], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    for (int s = 0; s < kSteps; ++s) {
+                        const uint32_t sel = s & 1 ? 0x7362 : 0x5140;
+                        uint32_t a0, a1, a2, a3;
+                        code_pairs<CODE>(__byte_perm(v[0][s >> 1], v[1][s >> 1], sel), a0, a1);
+                        code_pairs<CODE>(__byte_perm(v[2][s >> 1], v[3][s >> 1], sel), a2, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float t4[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma16816(t4, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nt][s][e] = fmaf(t4[e], vs, o[nt][s][e]);
+                        }
+                    }
                 }
             }
             __syncwarp();       // the stage is free for the next copies
@@ -343,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                 for (int s = 4; s < 32; s <<= 1) z[nt][e] += __shfl_xor_sync(kFull, z[nt][e], s);
                 if (g == 0) {
                     sm_m[warp][nt * 8 + 2 * tig + e] = m[nt][e];
-                    sm_z[warp][nt * 8 + 2 * tig + e] = z[nt][e];
+                    sm_z[warp][nt * 8 + 2 * tig + e] = z[nt][e] * (128.f * kSumUnit);
                 }
             }
         __syncthreads();
@@ -354,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * tig + e;
                 const float mm = fmaxf(fmaxf(sm_m[0][row], sm_m[1][row]), fmaxf(sm_m[2][row], sm_m[3][row]));
-                const float f = ex2(m[nt][e] - mm) * (vref * (1.f / 128.f));
+                const float f = ex2(m[nt][e] - mm);
                 float *dst = obuf + (warp * kRows + row) * D + g * (D / 8);
 #pragma unroll
                 for (int s = 0; s < kSteps; s += 2)

@@ -25,21 +25,25 @@ def _cu(n):
     return [0, *torch.tensor(n).cumsum(0).tolist()]
 
 
-def exact(q, pools, table, lens, nq, scale, window, page, qmax):
+def exact(q, pools, table, lens, nq, scale, window, page):
     """(out, bound before the last rounding) in 64 bits, from the definition: a row sees what its
     mask and the readable pages leave, nothing else touches it, whatever it is.
 
-    Bound: a weight p_j is rounded to fp16, by 2^-11 of itself or, below fp16's normal numbers,
-    by 2^-32 of the row's largest (times 2^7, half a step of 2^-24).  The second kind only meets
-    values whose page's scale is at most 2^10 times the smallest one's, so |v| <= qmax 2^10 smin:
-    2^-22 qmax smin a token.  A logit is a sum of D products in fp32 with two scales on it, off
-    by (D + 8) 2^-23 of the sum of magnitudes (twice the rounding unit, for sums that the matrix
-    instructions truncate) and so is p_j, twice: as a summand and in the sum of weights.  2^-15: a
-    scale's logarithm beside the logit (up to 128, so 2^-18) and the running sums."""
+    Bound.  A weight p_j is rounded to fp16 as P = 2^7 p_j / (the largest so far): by 2^-11 of
+    itself or, where P is below fp16's normal numbers, by half a step of 2^-24, at most P:
+    min(p_j, 2^-32 of the largest).  The largest is that of the keys that a warp of the kernel for
+    few rows has met, none of whose value scales is below 2^-10 of this key's (else the product is
+    formed in fp32).  The kernel for many rows takes p_j times the value scale in place of p_j, of
+    scales within 2^10: 2^-22 in place of 2^-32.
+    A logit is a sum of D products in fp32 with two scales on it, off by (D + 8) 2^-23 of the sum of
+    magnitudes (twice the rounding unit, for sums that the matrix instructions truncate) and so is
+    p_j, twice: as a summand and in the sum of weights.  2^-15: a scale's logarithm beside the logit
+    (up to 128, so 2^-18) and the running sums."""
     kp, vp, ks, vs = (t.cpu() for t in pools)
     T, Hq, D = q.shape
     hkv = kp.shape[1]
     g = Hq // hkv
+    floor = 2.0 ** -32 if g * max(nq) <= 32 else 2.0 ** -22
     out, tol = torch.zeros((T, Hq, D), dtype=F64), torch.zeros((T, Hq, D), dtype=F64)
     cu = _cu(nq)
     for b, (n, L) in enumerate(zip(nq, lens)):
@@ -60,15 +64,17 @@ def exact(q, pools, table, lens, nq, scale, window, page, qmax):
                 s = vs[ps, h].to(F64)
                 k = kp[ps, h, js % page].float().to(F64) * ks[ps, h].to(F64)[:, None]
                 v = vp[ps, h, js % page].float().to(F64) * s[:, None]
-                smin = s[s > 0].min().item() if (s > 0).any() else 0.0
                 qq = q[cu[b] + i, h * g:(h + 1) * g].to(F64)
                 p = torch.softmax(qq @ k.T * scale, -1)
                 d = 2 * (qq.abs() @ k.abs().T) * abs(scale) * (D + 8) * 2.0 ** -23
+                lost = torch.zeros_like(p)
+                for u in s.unique().tolist():
+                    most = p[:, s >= u / 1024].amax(-1, keepdim=True)
+                    lost[:, s == u] = torch.minimum(p[:, s == u], floor * most)
                 o = p @ v
                 out[cu[b] + i, h * g:(h + 1) * g] = o
-                tol[cu[b] + i, h * g:(h + 1) * g] = ((p * (2.0 ** -11 + 2.0 ** -15 + d)) @ v.abs() +
-                                                     (p * d).sum(-1, keepdim=True) * o.abs() +
-                                                     len(js) * 2.0 ** -22 * p.amax(-1, keepdim=True) * smin * qmax)
+                tol[cu[b] + i, h * g:(h + 1) * g] = ((p * (2.0 ** -11 + 2.0 ** -15 + d) + lost) @ v.abs() +
+                                                     (p * d).sum(-1, keepdim=True) * o.abs())
     return out, tol
 
 
@@ -107,7 +113,7 @@ def test_tokens_that_the_table_has_no_room_for_count_as_masked(length, nq, windo
         c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), d ** -0.5, cu=_i32(_cu(rows)).cuda(), max_q=nq, window=window,
                     out=out)
         assert c.poll_error() == tkv.TKV_ERR_CAPACITY
-        check(out, *exact(q, pools, table, lens, rows, d ** -0.5, window, page, 448.0), BF16)
+        check(out, *exact(q, pools, table, lens, rows, d ** -0.5, window, page), BF16)
 
 
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 30, 1 << 30, (1 << 30) - 1, 7])
@@ -123,4 +129,83 @@ def test_windows_without_an_end_and_rows_at_negative_positions(window, lens, nq)
     c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), d ** -0.5, cu=_i32(_cu(nq)).cuda(), max_q=max(nq), window=window,
                 out=out)
     assert c.poll_error() == tkv.TKV_OK
-    check(out, *exact(q, pools, table, lens, nq, d ** -0.5, window, page, 127.0), FP16)
+    check(out, *exact(q, pools, table, lens, nq, d ** -0.5, window, page), FP16)
+
+
+# ------------------------------------------------------------------ value scales far apart
+def _scales_apart(gen, kind, r, odd, page, hkv, d, code):
+    """Four pages in the sequence's order, of which page `odd` has a value scale 2^r times the
+    others'.  Dim 0 of the keys pushes a token down: by 1.02 (d 128) or 1.44 log2 units a code."""
+    big = 60 if code == "e4m3" else 24
+    to = po.TORCH_CODE[code]
+    k = (torch.randn((4, hkv, page, d), generator=gen) * 4).round()
+    v = (torch.randn((4, hkv, page, d), generator=gen) * big).clamp(-po.QMAX[code], po.QMAX[code]).round()
+    k[..., 0] = 0
+    vs = torch.full((4, hkv), 2.0 ** -6)
+    vs[odd] *= 2.0 ** r
+    if kind == "far":             # nobody attends to that page
+        k[odd, :, :, 0] = -96
+    elif kind == "holds_all":     # all the attention is on that page
+        k[:, :, :, 0] = -96
+        k[odd, :, :, 0] = 0
+    elif kind == "outlier":       # one token has set the page's scale, the others' values are zeros there
+        v[odd] = 0
+        v[odd, :, 5] = po.QMAX[code]
+        k[odd, :, 5, 0] = -96
+    else:                         # little weight, but values so large that they are the output
+        k[odd, :, :, 0] = -40
+    return k.to(to), v.to(to), torch.full((4, hkv), 2.0 ** -3), vs
+
+
+@pytest.mark.parametrize("kind,r", [("far", 24), ("far", 28), ("far", 34), ("far", 60), ("far", -40), ("holds_all", -24),
+                                    ("holds_all", -28), ("holds_all", -34), ("holds_all", -70), ("holds_all", 70),
+                                    ("outlier", 8), ("outlier", 20), ("outlier", 34), ("outlier", 90), ("little", 70),
+                                    ("little", 90)])
+@pytest.mark.parametrize("odd", [0, 2])
+@pytest.mark.parametrize("code,dtype,page,d", [("e4m3", BF16, 16, 128), ("int8", BF16, 64, 128), ("e4m3", BF16, 64, 64)])
+@pytest.mark.parametrize("nq,g", [(1, 4), (5, 2), (12, 2)])
+def test_value_scales_far_apart(kind, r, odd, code, dtype, page, d, nq, g):
+    gen = torch.Generator().manual_seed(abs(r) + odd)
+    hkv, L = 2, 4 * page - 3
+    k, v, ks, vs = _scales_apart(gen, kind, r, odd, page, hkv, d, code)
+    order = torch.tensor([2, 0, 3, 1])
+    pools = tuple(torch.empty_like(t.view(torch.uint8) if t.element_size() == 1 else t) for t in (k, v, ks, vs))
+    for dst, src in zip(pools, (k, v, ks, vs)):
+        dst[order] = src.view(torch.uint8) if src.element_size() == 1 else src
+    pools = tuple(p.view(s.dtype).cuda() for p, s in zip(pools, (k, v, ks, vs)))
+    table = order.to(torch.int32)[None]
+    q = torch.randn((nq, hkv * g, d), generator=gen)
+    q[..., 0] = 64
+    q = q.to(dtype)
+    want, tol = exact(q, pools, table, [L], [nq], d ** -0.5, 0, page)
+    # once, every unit of keys in another block; and many times, whole sequences in a block
+    for n in (1, 300):
+        c = TkvPagedCache(n, hkv, g, d, page, 4, 4, code=code, dtype=dtype, pools=pools)
+        cu = torch.arange(n + 1, dtype=torch.int32) * nq
+        out = c.attention(q.repeat(n, 1, 1).cuda(), table.repeat(n, 1).cuda(), _i32([L] * n).cuda(), d ** -0.5, cu=cu.cuda(),
+                          max_q=nq)
+        assert c.poll_error() == tkv.TKV_OK
+        for i in {0, 1, n // 2, n - 1}:
+            if i < n:
+                check(out[i * nq:(i + 1) * nq], want, tol, dtype)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("nq,g", [(1, 4), (5, 2), (12, 2)])
+def test_one_huge_value_does_not_reach_the_other_pages(code, nq, g):
+    """A sequence appended with one value of 2^34 among values near one: rows of other tokens' values
+    keep theirs, at decode and in chunks, over several blocks' parts."""
+    gen = torch.Generator().manual_seed(3)
+    page, hkv, d, L = 64, 2, 128, 3000
+    k, v = (torch.randn((L, hkv, d), generator=gen).to(BF16) for _ in range(2))
+    k[1234, :, 0] = -300.0
+    v[1234, :, 3] = 2.0 ** 34
+    c = TkvPagedCache(1, hkv, g, d, page, 48, 48, code=code)
+    table = torch.randperm(48, generator=gen).to(torch.int32)[None]
+    c.append(k.cuda(), v.cuda(), table.cuda(), _i32([L]).cuda(), cu=_i32([0, L]).cuda(), max_new=L)
+    q = torch.randn((nq, hkv * g, d), generator=gen)
+    q[..., 0] = 8.0
+    q = q.to(BF16)
+    out = c.attention(q.cuda(), table.cuda(), _i32([L]).cuda(), d ** -0.5, cu=_i32([0, nq]).cuda(), max_q=nq)
+    pools = (c.k_pool, c.v_pool, c.k_scale, c.v_scale)
+    check(out, *exact(q, pools, table, [L], [nq], d ** -0.5, 0, page), BF16)
