@@ -488,10 +488,17 @@ typedef struct {
 
 /* GQA attention of T query rows over the cache.  Row i of the n rows of sequence b is at
  * position p = kv_len[b] - n + i and sees keys max(0, p - window + 1) .. p (window 0: all
- * keys up to p):  out = sum_j softmax_j(softmax_scale * q . k_j) v_j, rounded once; a row
- * that sees no key (one at a negative position too) gives zeros, whatever is in q.  Tokens
- * of a page that cannot be read (see above) count as masked.  A NaN among a token's E4M3
- * values may reach the rows of its sequence in the same call that come before it. */
+ * keys up to p):  out = sum_j softmax_j(softmax_scale * q . k_j) v_j; a row that sees no key
+ * (one at a negative position too) gives zeros, whatever is in q.  Tokens of a page that
+ * cannot be read (see above) count as masked.  out may be q.
+ * Products and sums are in fp32 with one rounding at the end, but for the operands of the
+ * matrix instructions, which are fp16: elements of a bf16 query are exact down to 2^-25 of the
+ * row's largest and multiples of 2^-32 of it below; a softmax weight is rounded to 11 bits and,
+ * up to 32 rows (G * max_q), to a multiple of 2^-31 of the row's largest weight, with more rows
+ * of 2^-21.  Value scales that differ by more than 2^10 within what a row sees do not change
+ * that, but are slower: up to 32 rows 1.7 times the time where half the keys' scales are that
+ * much above the others, with more rows about 200 times for such a sequence and head.
+ * A NaN among a token's E4M3 values may reach the rows of its sequence in the same call that come before it. */
 TKV_API tkv_status tkv_paged_attention(tkv_paged *cache, const tkv_paged_attention_args *args, void *stream);
 
 /* As tkv_poll_error and tkv_launch_count, for a paged cache. */

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
 
     long long begin, share;
     make_plan<kThreads>(a, plan, kUnitLog2, &begin, &share);
-    if (tid == 0) a.cut[blockIdx.x].parts = 0;
+    if (tid == 0) a.cut[blockIdx.x] = CutItem{};
     if (begin >= plan.total) return;
     const long long end = min(begin + share, plan.total);
     Cursor k;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
         }
         if (parts > kOwnParts) {
             if (tid == 0 && blockIdx.x == cut.first)
-                a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts};
+                a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, (int16_t)tokens, (int16_t)parts, 0};
         } else if (parts > 1) {
             __threadfence();
             __syncthreads();

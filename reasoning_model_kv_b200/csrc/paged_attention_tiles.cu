@@ -11,8 +11,12 @@
 // converting a key costs 1/256 of a row's work.
 // A page's two scales enter as y = x + log2(value scale) in place of the logit x: P = 2^(y - M)
 // carries the value scale, O = sum P code, and the softmax sum is sum P / value scale, so both
-// have one running maximum M, which moves only when y passes it by 2^8.  P is fp16 times 2^7
-// (11 bits, more than either output type keeps; down to 2^-31 of the largest).
+// have one running maximum M, which moves only when y passes it by 2^8.  P is fp16 times 2^7:
+// 11 bits, more than either output type keeps, and multiples of 2^-31 of the largest.  So an
+// attended key of a page with a large scale, even one whose codes are zeros, takes bits from the
+// others: 2^10 between an item's scales leave 2^-21 of the largest weight.  Rows of items whose
+// scales are further apart are formed in fp32 by the join kernel, which follows anyway; a warp of
+// its own looks for them (looked for by the softmax or the codes' warps, they cost 1 to 5 %).
 //
 // Measured: two chunks of 2048 rows x 32 heads on 14k and 16k keys, 961 GFLOP, in 925 us = 1.04
 // PFLOP/s, 63 % of the library's bf16 product.  Tensor cores and exponentials are each busy 46 %
@@ -20,6 +24,8 @@
 // covers only part of that.  Slower: two threads a row (16 softmax warps), the maximum and P in
 // one pass with a second one where the maximum moved, an issuing warp for each tile of rows (its
 // products take turns with the other's; 312 -> 380 us on 2048 rows x 16 heads x 8k keys).
+#include <climits>
+
 #include <cuda_fp8.h>
 
 #include "f32x2.cuh"
@@ -38,10 +44,12 @@ using attn::mbar_arrive;
 using attn::mbar_wait;
 using attn::smem_addr;
 
-constexpr int kThreads = 512, kUnitLog2 = 7, kUnit = 128;
+constexpr int kThreads = 512, kUnitLog2 = kTileUnitLog2, kUnit = 1 << kUnitLog2;
 constexpr int kItemCost = 2;             // an item's setup takes about as long as this many units
 constexpr int kChunks = kUnit / 16;      // groups of keys that share a page
 constexpr int kConstSets = 4;
+// Items whose value scales are further apart, or larger, are left to the join kernel's plain rows.
+constexpr float kScaleSpread = 1024.f, kScaleMost = 1048576.f;
 constexpr float kTiny = 1e-37f;          // factors of logits stay above zero: -inf times one is -inf
 constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of tile s at 128 s, O at 256 + 128 s
 
@@ -74,6 +82,22 @@ __device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) 
     return __all_sync(kFull, mbar_wait(smem_addr(bar), parity));
 }
 
+// A count in shared memory that one warp raises: what it did before is seen behind the wait, which is
+// bounded as those on barriers are.
+__device__ __forceinline__ void store_release(uint32_t *count, uint32_t n) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(count)), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool wait_above(const uint32_t *count, uint32_t n) {
+    auto above = [&] {
+        uint32_t v;
+        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(count)) : "memory");
+        return v > n;
+    };
+    bool there = above();
+    for (const long long t0 = clock64(); !there && clock64() - t0 <= attn::kWaitCycles;) there = above();
+    return __all_sync(kFull, there);
+}
+
 __device__ __forceinline__ void st128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -94,6 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     __shared__ __align__(8) Barriers bar;
     __shared__ ChunkConst consts[kConstSets][kChunks];
     __shared__ uint32_t tmem_base;
+    __shared__ int plain_from;                // number of the first item that is left to the join
+    __shared__ uint32_t items_read;           // items whose scales have been looked through
     const View &c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -113,6 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         for (int i = 0; i < kConstSets; ++i) tc::mbar_init(&bar.c_full[i], 4);
         tc::mbar_init(&bar.drain, 1);
         tc::mbar_init_fence();
+        plain_from = INT_MAX;
+        items_read = 0;
+        a.cut[blockIdx.x] = CutItem{};
     }
     if (warp == 12) tc::alloc(smem_addr(&tmem_base), 512);
     long long begin, share;
@@ -123,9 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const uint32_t tb = tmem_base;
     const long long end = min(begin + share, plan.total);
     bool ok = true;
-    if (begin >= plan.total) {
-        if (tid == 0) a.cut[blockIdx.x].parts = 0;
-    } else {
+    if (begin < plan.total) {
         Cursor k;
         cursor_start(a, plan, begin, kUnitLog2, &k);
         uint32_t n_tile = 0, n_item = 0;          // units and items behind
@@ -137,7 +164,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;
             const uint32_t s_col = tb + lanes + kColS + 128 * sub, o_col = tb + lanes + kColO + 128 * sub;
             const int ti = row / c.G, hd = row - ti * c.G;
-            if (tid == 0) a.cut[blockIdx.x].parts = 0;
             do {
                 int u0, nu;
                 cursor_units(k, begin, end, &u0, &nu);
@@ -281,6 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     tc::fence_after();
                     const Parts cut = item_parts(k, share);
                     const int parts = cut.count;
+                    ok = wait_above(&items_read, n_item) && ok;
+                    const bool plain = *const_cast<volatile int *>(&plain_from) <= (int)n_item;
                     if (parts == 1) {
                         const float f = z > 0.f || z != z ? 1.f / z : 0.f;
                         T *dst = static_cast<T *>(const_cast<void *>(a.out.p)) + (long long)(k.s.row0 + k.i0 + tok) * a.out.token +
@@ -290,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                             uint32_t o[16];
                             tc::ld16(o_col + j, o);
                             tc::wait_ld<16>(o);
-                            if (live && ok) {
+                            if (live && ok && !plain) {
 #pragma unroll
                                 for (int e = 0; e < 16; e += 4)
                                     *reinterpret_cast<uint2 *>(dst + j + e) = make_uint2(
@@ -314,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         }
                         if (live) { p[r] = M; p[256 + r] = z; }
                         if (tid == 0 && blockIdx.x == cut.first)
-                            a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, tokens, parts};
+                            a.cut[blockIdx.x] = CutItem{k.s.row0 + k.i0, k.h * c.G, (int16_t)tokens, (int16_t)parts, 0};
                     }
                     tc::fence_before();      // the reads of O are behind the next item's products
                 }
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 };
                 ChunkConst cc0;
                 auto constants = [&] {
-                    const float v = fmaxf(vs0, 7.9e-31f);        // 2^-100: its codes count for nothing
+                    const float v = vs0 > 0.f ? vs0 : 8.271806e-25f;        // 2^-80, the least: its values are zeros
                     cc0 = id0 >= 0 ? ChunkConst{ks0 * sl, log2f(v), 1.f / v, 0.f} : ChunkConst{0.f, -INFINITY, 0.f, 0.f};
                 };
                 // a page's two groups of keys; values whose scale is zero are zeros
@@ -520,6 +548,33 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     release(&bar.drain);
                     warp_wait(&bar.drain, 0);
                 }
+            } else if (warp == 13) {
+                // ---- which items' value scales are too far apart
+                do {
+                    int u0, nu;
+                    cursor_units(k, begin, end, &u0, &nu);
+                    if (nu == 0) continue;
+                    const int t0 = max(k.r.lo, (k.r.tile0 + u0) << kUnitLog2), t1 = min(k.r.hi, (k.r.tile0 + u0 + nu) << kUnitLog2);
+                    float least = INFINITY, most = 0.f;
+#pragma unroll 4
+                    for (int p = (t0 >> c.page_log2) + lane; p < (t1 + c.page - 1) >> c.page_log2; p += 32) {
+                        uint32_t bad;
+                        const int id = load_page(c, a.block_table, k.b, p, &bad);
+                        const float vs = id >= 0 ? c.v_scale[(size_t)id * c.Hkv + k.h] : 0.f;
+                        least = fminf(least, vs > 0.f ? vs : INFINITY);
+                        most = fmaxf(most, vs);
+                    }
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) {
+                        least = fminf(least, __shfl_xor_sync(kFull, least, s));
+                        most = fmaxf(most, __shfl_xor_sync(kFull, most, s));
+                    }
+                    if (lane == 0) {
+                        if (most > kScaleSpread * least || most > kScaleMost) atomicMin(&plain_from, (int)n_item);
+                        store_release(&items_read, n_item + 1);
+                    }
+                    n_item += 1;
+                } while (cursor_next(a, kUnitLog2, end, &k));
             }
         }
         if (!ok && lane == 0) raise_error(c.err, kErrTimeout, kWaitTimeout);
@@ -527,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    if (tid == 0 && plain_from != INT_MAX) a.cut[blockIdx.x].plain = plain_from + 1;
     if (warp == 12) tc::dealloc(tb, 512);
 }
 

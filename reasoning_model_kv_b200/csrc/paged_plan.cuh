@@ -15,10 +15,13 @@
 namespace tkv {
 namespace paged {
 
-// The item that begins in a block's stretch and goes on in the next blocks'.
+// What a block leaves to the join: the item that begins in its stretch and goes on in the next
+// blocks', and where the items begin whose rows the join has to form by itself.
 struct CutItem {
-    int row0, head0, tokens;
-    int parts;              // blocks that hold a part; below 2: no such item
+    int row0, head0;
+    int16_t tokens;
+    int16_t parts;          // blocks that hold a part; below 2: no such item
+    int plain;              // 1 + number of the block's first such item (0: none)
 };
 
 struct AttnArgs {
@@ -105,7 +108,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warp_sum
 // Finds the block's stretch: *share places from *begin on (none if begin >= total), and where
 // that is.  Block 0 reports sequences that cannot be used, or whose last token (which their last
 // row sees) the block table has no room for.  All NT threads take part.
-template <int NT>
+template <int NT, bool REPORT = true>
 __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_log2, long long *begin, long long *share) {
     const int B = a.c.B, tid = threadIdx.x;
     long long sum = 0, mine = 0;
@@ -113,7 +116,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, Plan &p, int unit_l
         uint32_t bad;
         const Seq s = attention_seq(a, b, &bad);
         if (!bad && s.n > 0 && s.len > a.room) bad = kNoPage;
-        if (bad && blockIdx.x == 0) latch(a.c, bad);
+        if (REPORT && bad && blockIdx.x == 0) latch(a.c, bad);
         mine = head_units(a, s, unit_log2) * a.c.Hkv;
         sum += mine;
     }
