@@ -240,11 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         for (int j = 0; j < 128; j += 32) tc::ld32(s_col + j, s + j);
                         tc::wait_ld<128>(s);
                         const int t0 = (k.r.tile0 + u0 + i) << kUnitLog2;
-                        if (t0 + kUnit - 1 > sub_first || (a.window && t0 <= sub_last - a.window)) {
+                        // (keys without a page are zeros, and S is NaN there if the query is not finite)
+                        float least = lb[0];
+#pragma unroll
+                        for (int j = 1; j < SETS; ++j) least = fminf(least, lb[j]);
+                        if (t0 + kUnit - 1 > sub_first || (a.window && t0 <= sub_last - a.window) || least == -INFINITY) {
                             const int hi = pos - t0, lo = a.window ? hi - a.window : -1;      // lo < key <= hi
 #pragma unroll
                             for (int j = 0; j < 128; ++j)
-                                if (j > hi || j <= lo) s[j] = 0xff800000u;
+                                if (j > hi || j <= lo || lb[j / kKeys] == -INFINITY) s[j] = 0xff800000u;
                         }
                         float ym = -INFINITY;
 #pragma unroll

@@ -244,3 +244,24 @@ def test_scales_apart_in_some_sequences_and_outputs_over_the_queries(page, g, wi
     for b in (0, 1, 7, 21, 39):
         want, tol = exact(q[cu[b]:cu[b + 1]], pools, table[b:b + 1], lens[b:b + 1], nq[b:b + 1], d ** -0.5, window, page)
         check(out[cu[b]:cu[b + 1]], want, tol, dtype)
+
+
+# ------------------------------------------------------------------ what is not finite
+@pytest.mark.parametrize("nq", [1, 5, 45])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_queries_that_are_not_finite_over_pages_that_cannot_be_read(nq, page, value):
+    """No key that such a row may see can be read: zeros, as for any row that sees none.  The next
+    sequence, some of whose pages are missing, keeps its own values."""
+    gen = torch.Generator().manual_seed(nq)
+    hkv, g, d = 1, 4, 128
+    pools = _small_pools(gen, 8, hkv, page, d, "e4m3")
+    table = _i32([[-1, -1, -1, -1], [0, -1, 3, 7]])
+    lens, rows = [4 * page - 1, 4 * page - 2], [nq, nq]
+    q = torch.randn((2 * nq, hkv * g, d), generator=gen).to(BF16)
+    q[:nq] = value
+    c = TkvPagedCache(2, hkv, g, d, page, 8, 4, pools=pools)
+    out = c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), d ** -0.5, cu=_i32(_cu(rows)).cuda(), max_q=nq)
+    assert c.poll_error() == tkv.TKV_ERR_CAPACITY
+    assert (out[:nq] == 0).all()
+    check(out, *exact(q, pools, table, lens, rows, d ** -0.5, 0, page), BF16)
