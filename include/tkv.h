@@ -498,7 +498,8 @@ typedef struct {
  * of 2^-21.  Value scales that differ by more than 2^10 within what a row sees do not change
  * that, but are slower: up to 32 rows 1.7 times the time where half the keys' scales are that
  * much above the others, with more rows about 200 times for such a sequence and head.
- * A NaN among a token's E4M3 values may reach the rows of its sequence in the same call that come before it. */
+ * A NaN among a token's E4M3 values reaches the rows that see the token and no others; with
+ * more than 32 rows it is as slow where some of them see it. */
 TKV_API tkv_status tkv_paged_attention(tkv_paged *cache, const tkv_paged_attention_args *args, void *stream);
 
 /* As tkv_poll_error and tkv_launch_count, for a paged cache. */

@@ -82,7 +82,8 @@ struct Stage {
 };
 
 // o += P V of 16 keys in fp32: the lane's rows 2 tig, 2 tig + 1 of every row tile and its D / 8 dims,
-// which are 16 (8) codes of every key.  p as the products S left it, f the values' factor.
+// which are 16 (8) codes of every key.  p as the products S left it, below 0 where the row does not
+// see the key (whose value may be NaN), f the values' factor.
 template <int D, int CODE, int NT>
 __device__ __forceinline__ void plain_values(uint32_t vt, float f, const float (&p)[NT][4], float (&o)[NT][D / 16][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
@@ -102,7 +103,7 @@ __device__ __forceinline__ void plain_values(uint32_t vt, float f, const float (
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) pj[nt][e] = __shfl_sync(kFull, p[nt][e + 2 * half], 4 * j + tig) * f;
+                for (int e = 0; e < 2; ++e) pj[nt][e] = __shfl_sync(kFull, p[nt][e + 2 * half], 4 * j + tig);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t c[2];
@@ -114,8 +115,9 @@ __device__ __forceinline__ void plain_values(uint32_t vt, float f, const float (
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            o[nt][2 * i + k][e] = fmaf(pj[nt][e], v.x, o[nt][2 * i + k][e]);
-                            o[nt][2 * i + k][e + 2] = fmaf(pj[nt][e], v.y, o[nt][2 * i + k][e + 2]);
+                            if (pj[nt][e] < 0.f) continue;
+                            o[nt][2 * i + k][e] = fmaf(pj[nt][e] * f, v.x, o[nt][2 * i + k][e]);
+                            o[nt][2 * i + k][e + 2] = fmaf(pj[nt][e] * f, v.y, o[nt][2 * i + k][e + 2]);
                         }
                 }
             }
@@ -281,6 +283,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
             for (int s = 0; s < kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
         }
         const int last_pos = k.r.first + tokens - 1;
+        // Is element e of row tile nt's products with the 16 keys from t on outside its row's sight?
+        auto hidden = [&](int nt, int e, int t) {
+            const int pos = k.r.first + (nt * 8 + 2 * tig + (e & 1)) / c.G, j = t + g + 8 * (e >> 1);
+            return j > pos || (a.window && j <= pos - a.window);
+        };
         lower(vs0);
         lower(vs1);
 #pragma unroll
@@ -321,10 +328,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                     x[nt][0] *= f0; x[nt][1] *= f1; x[nt][2] *= f0; x[nt][3] *= f1;
                     if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int pos = k.r.first + (nt * 8 + 2 * tig + (e & 1)) / c.G, j = t + g + 8 * (e >> 1);
-                            if (j > pos || (a.window && j <= pos - a.window)) x[nt][e] = -INFINITY;
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (hidden(nt, e, t)) x[nt][e] = -INFINITY;
                     }
                     up |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + attn::kRescaleSlack ||
                           fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + attn::kRescaleSlack;
@@ -353,7 +358,25 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
                     z[nt][0] += p[nt][0] + p[nt][2];
                     z[nt][1] += p[nt][1] + p[nt][3];
                 }
-                if (info.wide) {
+                bool plain = info.wide;
+                if (CODE == TKV_CODE_E4M3 && edge) {
+                    // a NaN of a key that some rows do not see: zero times it would be NaN
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < kTile / 512; ++i) {
+                        const uint4 w = lds128(vt + i * 512 + lane * 16);
+                        nan |= any_nan_code(w.x) || any_nan_code(w.y) || any_nan_code(w.z) || any_nan_code(w.w);
+                    }
+                    if (__any_sync(kFull, nan)) {
+                        plain = true;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (hidden(nt, e, t)) p[nt][e] = -1.f;
+                    }
+                }
+                if (plain) {
                     plain_values<D, CODE, NT>(vt, vs * 128.f, p, o);
                 } else {
                     uint32_t pb[NT][2];

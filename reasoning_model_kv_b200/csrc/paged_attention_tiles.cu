@@ -15,8 +15,10 @@
 // 11 bits, more than either output type keeps, and multiples of 2^-31 of the largest.  So an
 // attended key of a page with a large scale, even one whose codes are zeros, takes bits from the
 // others: 2^10 between an item's scales leave 2^-21 of the largest weight.  Rows of items whose
-// scales are further apart are formed in fp32 by the join kernel, which follows anyway; a warp of
-// its own looks for them (looked for by the softmax or the codes' warps, they cost 1 to 5 %).
+// scales are further apart are formed in fp32 by the join kernel, which follows anyway, and so are
+// those of items with a NaN value that some rows see and others do not (zero times it would be
+// NaN); warps of their own look for them (the softmax's or the codes' warps would take 1 to 5 %
+// longer).
 //
 // Measured: two chunks of 2048 rows x 32 heads on 14k and 16k keys, 961 GFLOP, in 925 us = 1.04
 // PFLOP/s, 63 % of the library's bf16 product.  Tensor cores and exponentials are each busy 46 %
@@ -48,7 +50,8 @@ constexpr int kThreads = 512, kUnitLog2 = kTileUnitLog2, kUnit = 1 << kUnitLog2;
 constexpr int kItemCost = 2;             // an item's setup takes about as long as this many units
 constexpr int kChunks = kUnit / 16;      // groups of keys that share a page
 constexpr int kConstSets = 4;
-// Items whose value scales are further apart, or larger, are left to the join kernel's plain rows.
+constexpr int kReaders = 3;              // warps that look for what is left to the join kernel's plain rows
+// Items whose value scales are further apart, or larger, are.
 constexpr float kScaleSpread = 1024.f, kScaleMost = 1048576.f;
 constexpr float kTiny = 1e-37f;          // factors of logits stay above zero: -inf times one is -inf
 constexpr uint32_t kColS = 0, kColO = 256;      // tensor memory: S of tile s at 128 s, O at 256 + 128 s
@@ -82,15 +85,17 @@ __device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) 
     return __all_sync(kFull, mbar_wait(smem_addr(bar), parity));
 }
 
-// A count in shared memory that one warp raises: what it did before is seen behind the wait, which is
-// bounded as those on barriers are.
+// Counts in shared memory that a warp each raises: what they did before is seen behind the wait, which
+// is bounded as those on barriers are.
 __device__ __forceinline__ void store_release(uint32_t *count, uint32_t n) {
     asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(count)), "r"(n) : "memory");
 }
-__device__ __forceinline__ bool wait_above(const uint32_t *count, uint32_t n) {
+template <int N>
+__device__ __forceinline__ bool wait_above(const uint32_t (&count)[N], uint32_t n) {
+    const uint32_t at = smem_addr(count + (threadIdx.x & 31) % N);
     auto above = [&] {
         uint32_t v;
-        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(count)) : "memory");
+        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
         return v > n;
     };
     bool there = above();
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     __shared__ ChunkConst consts[kConstSets][kChunks];
     __shared__ uint32_t tmem_base;
     __shared__ int plain_from;                // number of the first item that is left to the join
-    __shared__ uint32_t items_read;           // items whose scales have been looked through
+    __shared__ uint32_t items_read[kReaders]; // items that each reader has looked through
     const View &c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         tc::mbar_init(&bar.drain, 1);
         tc::mbar_init_fence();
         plain_from = INT_MAX;
-        items_read = 0;
+        for (int i = 0; i < kReaders; ++i) items_read[i] = 0;
         a.cut[blockIdx.x] = CutItem{};
     }
     if (warp == 12) tc::alloc(smem_addr(&tmem_base), 512);
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     tc::fence_after();
                     const Parts cut = item_parts(k, share);
                     const int parts = cut.count;
-                    ok = wait_above(&items_read, n_item) && ok;
+                    ok = wait_above<kReaders>(items_read, n_item) && ok;
                     const bool plain = *const_cast<volatile int *>(&plain_from) <= (int)n_item;
                     if (parts == 1) {
                         const float f = z > 0.f || z != z ? 1.f / z : 0.f;
@@ -552,16 +557,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                     release(&bar.drain);
                     warp_wait(&bar.drain, 0);
                 }
-            } else if (warp == 13) {
-                // ---- which items' value scales are too far apart
+            } else {
+                // ---- which items the join has to form: the first reader goes through the value scales,
+                // all of them through the codes of the keys that not all rows see
+                const int reader = warp - 13;
                 do {
                     int u0, nu;
                     cursor_units(k, begin, end, &u0, &nu);
                     if (nu == 0) continue;
                     const int t0 = max(k.r.lo, (k.r.tile0 + u0) << kUnitLog2), t1 = min(k.r.hi, (k.r.tile0 + u0 + nu) << kUnitLog2);
+                    bool plain = false;
+                    if (CODE == TKV_CODE_E4M3) {
+                        constexpr int kLanes = D / 16, kStep = 32 * kReaders / kLanes;      // a key's lanes; keys at once
+                        const int of = reader * 32 + lane, last = k.r.first + min(a.tile_tokens, k.s.n - k.i0) - 1;
+                        auto read = [&](int j0, int j1) {
+#pragma unroll 4
+                            for (int j = j0 + of / kLanes; j < j1; j += kStep) {
+                                uint32_t bad;
+                                const int id = load_page(c, a.block_table, k.b, j >> c.page_log2, &bad);
+                                if (id < 0) continue;
+                                const size_t row = (((size_t)id * c.Hkv + k.h) << c.page_log2) + (j & (c.page - 1));
+                                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(c.v_pool + row * D + of % kLanes * 16));
+                                plain |= any_nan_code(w.x) || any_nan_code(w.y) || any_nan_code(w.z) || any_nan_code(w.w);
+                            }
+                        };
+                        read(max(t0, k.r.first + 1), t1);
+                        if (a.window) read(t0, min(t1, min(last - a.window, k.r.first) + 1));
+                    }
                     float least = INFINITY, most = 0.f;
 #pragma unroll 4
-                    for (int p = (t0 >> c.page_log2) + lane; p < (t1 + c.page - 1) >> c.page_log2; p += 32) {
+                    for (int p = reader > 0 ? INT_MAX : (t0 >> c.page_log2) + lane; p < (t1 + c.page - 1) >> c.page_log2; p += 32) {
                         uint32_t bad;
                         const int id = load_page(c, a.block_table, k.b, p, &bad);
                         const float vs = id >= 0 ? c.v_scale[(size_t)id * c.Hkv + k.h] : 0.f;
@@ -573,9 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         least = fminf(least, __shfl_xor_sync(kFull, least, s));
                         most = fmaxf(most, __shfl_xor_sync(kFull, most, s));
                     }
+                    plain = __any_sync(kFull, plain) || most > kScaleSpread * least || most > kScaleMost;
                     if (lane == 0) {
-                        if (most > kScaleSpread * least || most > kScaleMost) atomicMin(&plain_from, (int)n_item);
-                        store_release(&items_read, n_item + 1);
+                        if (plain) atomicMin(&plain_from, (int)n_item);
+                        store_release(items_read + reader, n_item + 1);
                     }
                     n_item += 1;
                 } while (cursor_next(a, kUnitLog2, end, &k));

@@ -7,6 +7,9 @@
 namespace tkv {
 namespace paged {
 
+// Is one of a word's four codes an E4M3 NaN (all bits but the sign's)?
+__device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
+
 // Codes 0, 1 (lo) and 2, 3 (hi) of a word: E4M3 through the hardware's conversion, integers as
 // 0x6400 | (code + 128), which is 1024 + 128 + code in fp16, less 1152.
 template <int CODE>

@@ -265,3 +265,31 @@ def test_queries_that_are_not_finite_over_pages_that_cannot_be_read(nq, page, va
     assert c.poll_error() == tkv.TKV_ERR_CAPACITY
     assert (out[:nq] == 0).all()
     check(out, *exact(q, pools, table, lens, rows, d ** -0.5, 0, page), BF16)
+
+
+@pytest.mark.parametrize("nq", [1, 3, 12, 45, 150])
+@pytest.mark.parametrize("window", [0, 20, 100])
+@pytest.mark.parametrize("page,d", [(16, 128), (64, 64), (64, 128)])
+def test_values_that_are_nan_reach_the_rows_that_see_them_only(nq, window, page, d):
+    """NaN among the values or the keys of tokens that some rows of a call see and others do not,
+    before the rows' first token and behind it, or outside a window."""
+    gen = torch.Generator().manual_seed(nq + window)
+    hkv, g, lens = 2, 2, [333, 200]
+    mp = -(-max(lens) // page)
+    pools = _small_pools(gen, 2 * mp, hkv, page, d, "e4m3")
+    table = torch.randperm(2 * mp, generator=gen).to(torch.int32).view(2, mp)
+
+    def poison(pool, b, j, h, dims):
+        pool.view(torch.uint8)[int(table[b, j // page]), h, j % page, dims] = 0xff
+
+    poison(pools[1], 0, 333 - 2, 0, slice(3, 7))
+    poison(pools[1], 0, max(0, 333 - nq // 2 - window), 0, slice(d - 1, d))
+    poison(pools[1], 0, 333 - nq // 3 - 20, 1, slice(0, d))
+    poison(pools[0], 1, 200 - nq // 2 - 1, 0, slice(5, 6))
+    poison(pools[1], 1, 200 - min(nq, 200) + nq // 3, 1, slice(8, 12))
+    c = TkvPagedCache(2, hkv, g, d, page, 2 * mp, mp, pools=pools)
+    q = torch.randn((2 * nq, hkv * g, d), generator=gen).to(BF16)
+    out = c.attention(q.cuda(), table.cuda(), _i32(lens).cuda(), d ** -0.5, cu=_i32([0, nq, 2 * nq]).cuda(), max_q=nq,
+                      window=window)
+    assert c.poll_error() == tkv.TKV_OK
+    check(out, *exact(q, pools, table, lens, [nq, nq], d ** -0.5, window, page), BF16)
