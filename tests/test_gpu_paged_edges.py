@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from reasoning_model_kv_b200 import TkvPagedCache, tkv
+from reasoning_model_kv_b200 import TkvPagedCache, TkvRope, tkv, tkv_qk_norm_rope
 from tests import paged_oracle as po
 from tests.conftest import gpu_available
 
@@ -293,3 +293,42 @@ def test_values_that_are_nan_reach_the_rows_that_see_them_only(nq, window, page,
                       window=window)
     assert c.poll_error() == tkv.TKV_OK
     check(out, *exact(q, pools, table, lens, [nq, nq], d ** -0.5, window, page), BF16)
+
+
+# ------------------------------------------------------------------ streams
+def _busy(n=40):
+    """Some milliseconds of work on the current stream."""
+    x = torch.zeros((8192, 8192), dtype=BF16, device="cuda")
+    for _ in range(n):
+        x = x @ x
+    return x
+
+
+@pytest.mark.parametrize("op", ["attention", "append", "norm_rope"])
+def test_outputs_of_another_stream_are_not_the_current_streams_memory(op):
+    """While the current stream still works on memory that the program has given back, a call on
+    another stream makes its output: the earlier work's late writes must not end up in it."""
+    gen = torch.Generator().manual_seed(1)
+    c = TkvPagedCache(64, 4, 4, 128, 64, 64, 1, pools=_small_pools(gen, 64, 4, 64, 128, "e4m3"))
+    q = torch.randn((64, 16, 128), generator=gen).to(BF16).cuda()
+    k = torch.randn((64, 4, 128), generator=gen).to(BF16).cuda()
+    table, lens, pos = torch.arange(64, dtype=torch.int32)[:, None].cuda(), _i32([40] * 64).cuda(), _i32(range(64)).cuda()
+    rope = TkvRope((10000.0 ** (-torch.arange(0, 128, 2) / 128)).cuda())
+    call = {"attention": lambda s: c.attention(q, table, lens, 0.1, stream=s),
+            "append": lambda s: c.append(k, k, table, lens, rope=rope, q=q, stream=s),
+            "norm_rope": lambda s: tkv_qk_norm_rope(q, k, pos, rope, stream=s)[0]}[op]
+    want = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        keep = _busy()
+        given_back = [torch.empty_like(q) for _ in range(8)]
+        for t in given_back:
+            t.fill_(9.0)                # runs when the products are done
+        del given_back, t
+        got = call(side)
+        side.synchronize()
+        first = got.clone()             # behind the current stream's work
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(first, want)
+        del keep, got
