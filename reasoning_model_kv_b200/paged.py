@@ -76,15 +76,10 @@ def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
 
 
 def _output(out, like: torch.Tensor, stream, name: str):
-    """(out, its address and strides): a new contiguous tensor of the rows' shape, or `out`.  Memory
-    comes from the stream that writes it: the current stream's may be what its unfinished work uses."""
+    """(out, its address and strides): a new contiguous tensor of the rows' shape, or `out`."""
     if out is None:
-        if stream is None:
-            out = torch.empty_like(like, memory_format=_CONTIGUOUS)
-        else:
-            with torch.cuda.stream(stream):
-                out = torch.empty_like(like, memory_format=_CONTIGUOUS)
-            out.record_stream(torch.cuda.current_stream(like.device))
+        out = (torch.empty_like(like, memory_format=_CONTIGUOUS) if stream is None else
+               tkv._empty(like.shape, like.dtype, like.device, stream))
         _, heads, dim = like.shape
         return out, (out.data_ptr(), heads * dim, dim)
     if out.shape != like.shape:

@@ -144,6 +144,17 @@ def tkv_workspace_bytes(cfg: TkvConfig) -> int:
     return lib().tkv_workspace_bytes(ctypes.byref(cfg))
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """Memory for an output that `stream` (None: the current one) writes, from that stream's pool:
+    the current stream's may be what its unfinished work uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _stream(stream=None) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -225,7 +236,7 @@ class TkvCache:
         if q.shape != (self.B, self.Hkv * self.G, 128):
             raise TkvError(TKV_ERR_INVALID, f"q must be [B, Hkv*G, 128], got {tuple(q.shape)}")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = _empty(q.shape, torch.float32, q.device, stream)
         _check(lib().tkv_decode_attention(self._h, _dptr(q, torch.bfloat16, "q"),
                                           float(softmax_scale), _dptr(out, torch.float32, "out"),
                                           _stream(stream)))
@@ -243,7 +254,7 @@ class TkvCache:
         if q.shape != (self.B, self.Hkv * self.G, 128):
             raise TkvError(TKV_ERR_INVALID, f"q must be [B, Hkv*G, 128], got {tuple(q.shape)}")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = _empty(q.shape, torch.float32, q.device, stream)
         _check(lib().tkv_decode_step(self._h, _dptr(k, torch.bfloat16, "k"), _dptr(v, torch.bfloat16, "v"),
                                      _dptr(cls, torch.uint8, "cls"), _dptr(pos, torch.int32, "pos"),
                                      _dptr(q, torch.bfloat16, "q"), float(softmax_scale),
@@ -258,9 +269,9 @@ class TkvCache:
         if q.shape != (self.B, self.Hkv * self.G, 128):
             raise TkvError(TKV_ERR_INVALID, f"q must be [B, Hkv*G, 128], got {tuple(q.shape)}")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        sp = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        cls = torch.empty(q.shape[:2], dtype=torch.uint8, device=q.device)
+            out = _empty(q.shape, torch.float32, q.device, stream)
+        sp = _empty(q.shape[:2], torch.float32, q.device, stream)
+        cls = _empty(q.shape[:2], torch.uint8, q.device, stream)
         _check(lib().tkv_decode_attention_sparsity(self._h, _dptr(q, torch.bfloat16, "q"), float(softmax_scale),
                                                    _dptr(out, torch.float32, "out"),
                                                    _dptr(sp, torch.float32, "sparsity"),

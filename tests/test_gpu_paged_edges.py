@@ -7,9 +7,11 @@ import math
 import pytest
 import torch
 
+import synth
 from reasoning_model_kv_b200 import TkvPagedCache, TkvRope, tkv, tkv_qk_norm_rope
 from tests import paged_oracle as po
 from tests.conftest import gpu_available
+from tests.gpu_harness import build_pair
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a CUDA device")]
@@ -331,4 +333,30 @@ def test_outputs_of_another_stream_are_not_the_current_streams_memory(op):
         first = got.clone()             # behind the current stream's work
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(first, want)
+        del keep, got
+
+
+@pytest.mark.parametrize("call", ["attention", "sparsity", "step"])
+def test_decode_outputs_of_another_stream_are_not_the_current_streams_memory(call):
+    """The same of the thought-adaptive cache's calls."""
+    w, gpu, _, _ = build_pair("tiny_b1_ctx2k")
+    state = gpu.export_state()
+    k, v, cls, pos, q = (t.cuda() for t in synth.decode_inputs(w, 0))
+    new = [t[:, :, 0].contiguous() for t in (k, v)] + [t[:, 0].contiguous() for t in (cls, pos)]
+    run = {"attention": lambda s: [gpu.decode_attention(q, 0.1, stream=s)],
+           "sparsity": lambda s: list(gpu.decode_attention_sparsity(q, 0.1, stream=s)),
+           "step": lambda s: [gpu.decode_step(*new, q, 0.1, stream=s)]}[call]
+    want = run(None)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        gpu.import_state(state)
+        torch.cuda.synchronize()
+        keep = _busy()
+        given_back = [torch.empty_like(x) for x in want for _ in range(8)]
+        for t in given_back:
+            t.fill_(9)
+        del given_back, t
+        got = run(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
         del keep, got
