@@ -169,7 +169,8 @@ class TkvPagedCache:
         self.B, self.Hkv, self.G, self.D, self.page, self.pages, self.max_pages = B, Hkv, G, D, page, pages, max_pages
         self.code, self.dtype = code, dtype
         shape = (pages, Hkv, page, D)
-        if pools is None:
+        made = pools is None
+        if made:
             device = torch.device(device)
             pools = (*(torch.zeros(shape, dtype=torch.uint8, device=device).view(CODES[code][1]) for _ in range(2)),
                      *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
@@ -197,6 +198,7 @@ class TkvPagedCache:
         self._append, self._attention = lib().tkv_paged_append, lib().tkv_paged_attention
         if share is None:
             self.reset()
+        if share is None or made:
             torch.cuda.current_stream(self.device).synchronize()    # ready for any stream
 
     def __del__(self):

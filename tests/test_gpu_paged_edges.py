@@ -360,3 +360,21 @@ def test_decode_outputs_of_another_stream_are_not_the_current_streams_memory(cal
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del keep, got
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_new_caches_pools_are_ready_for_any_stream(shared):
+    """Pools that a cache makes are zeroed when it is there, with a workspace of its own or shared:
+    what another stream appends at once stays."""
+    page, hkv, d = 16, 2, 64
+    first = TkvPagedCache(1, hkv, 1, d, page, 512, 4)
+    x = torch.ones((1, hkv, d), dtype=BF16, device="cuda")
+    table, lens = _i32([[3, 2, 1, 0]]).cuda(), _i32([1]).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    keep = _busy()
+    c = TkvPagedCache(1, hkv, 1, d, page, 512, 4, share=first if shared else None)
+    c.append(x, x, table, lens, stream=side)
+    torch.cuda.synchronize()
+    assert (c.k_pool[3, :, 0].float() * c.k_scale[3][:, None] == 1).all() and (c.v_scale[3] > 0).all()
+    del keep
