@@ -384,7 +384,8 @@ TKV_API int64_t tkv_launch_count(const tkv_cache *cache);
  * Rows before cu[0] and behind cu[B] are not read and their outputs are left as they were.
  * Row arrays (q, k, v and the outputs) are [rows][heads][D] of the configured type with a
  * contiguous head dim; token and head strides count elements, are multiples of 4 and the
- * arrays are 8-byte aligned.  Conditions only the device can see skip what they touch and
+ * arrays are 8-byte aligned.  An output's rows do not overlap: with several tokens and heads,
+ * a token's heads lie within one token stride, or a head's tokens within one head stride.  Conditions only the device can see skip what they touch and
  * latch an error for tkv_paged_poll_error: a page id of -1 or a table that is too short
  * TKV_ERR_CAPACITY; a page id outside [0, pages), cu that decreases or leaves [0, T] and
  * lengths below 0 TKV_ERR_INVALID.

@@ -63,8 +63,11 @@ const char *rows_fault(const Rows &r) {
 }
 const char *out_fault(const Rows &r, int T, int heads, int D) {
     if (const char *w = rows_fault(r)) return w;
-    // rows that overlap would be written by several threads
+    // rows that overlap would be written by several threads: a token's heads lie within its stride, or
+    // a head's tokens within that one's
     if ((heads > 1 && r.head < D) || (T > 1 && r.token < D)) return "output rows overlap";
+    if (heads > 1 && T > 1 && heads - 1 > (r.token - D) / r.head && T - 1 > (r.head - D) / r.token)
+        return "output rows overlap";
     return nullptr;
 }
 

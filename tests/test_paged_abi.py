@@ -146,3 +146,19 @@ def test_more_rows_than_positions_are_refused():
         assert L.tkv_paged_append(h, paged._APPEND_ARGS.pack(*row, *row, 0, 0, 0, 0, 0, 0, p, p, p, 0, T, 1), None) == INV
         assert L.tkv_paged_attention(h, paged._ATTENTION_ARGS.pack(*row, p, 1024, 128, p, p, p, T, 1, 0, 0.1), None) == INV
     assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_destroy(h) == 0
+
+
+def test_output_rows_that_overlap_across_tokens_and_heads_are_refused():
+    """Equal strides make (token 0, head 1) and (token 1, head 0) one row, and so on.  (Outputs with
+    heads before tokens, which do not overlap, are in the GPU tests.)"""
+    L, p = tkv.lib(), 1 << 24
+    h, row = _create(B=4), [p, 768, 128]
+    for strides in ((128, 128), (256, 128), (7 * 128, 128), (128, 256), (128, 384), (1 << 40, 1 << 38)):
+        out = [p, *strides]
+        args = [(L.tkv_paged_attention, h, paged._ATTENTION_ARGS.pack(p, 1024, 128, *out, p, p, 0, 4, 1, 0, 0.1)),
+                (L.tkv_paged_append, h, paged._APPEND_ARGS.pack(*row, *row, p, 1024, 128, *out, p, p, 0, 0, 4, 1)),
+                (L.tkv_qk_norm_rope, paged._NORM_ROPE_ARGS.pack(p, 1024, 128, *row, *out, *row, p, _rope(), 4, 8, 2, 128, 0)),
+                (L.tkv_qk_norm_rope, paged._NORM_ROPE_ARGS.pack(*row, p, 1024, 128, *row, *out, p, _rope(), 4, 2, 8, 128, 0))]
+        for fn, *a in args:
+            assert fn(*a, None) == INV and "overlap" in tkv.lib().tkv_last_error_string().decode(), strides
+    assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_destroy(h) == 0
