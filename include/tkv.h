@@ -388,7 +388,8 @@ TKV_API int64_t tkv_launch_count(const tkv_cache *cache);
  * a token's heads lie within one token stride, or a head's tokens within one head stride.  Conditions only the device can see skip what they touch and
  * latch an error for tkv_paged_poll_error: a page id of -1 or a table that is too short
  * TKV_ERR_CAPACITY; a page id outside [0, pages), cu that decreases or leaves [0, T] and
- * lengths below 0 TKV_ERR_INVALID.
+ * lengths below 0 TKV_ERR_INVALID.  Where cu decreases, two sequences may have the same rows:
+ * what is written for those is either's, or nothing.
  * ------------------------------------------------------------------------- */
 enum { TKV_CODE_INT8 = 0, TKV_CODE_E4M3 = 1 };
 enum { TKV_DTYPE_BF16 = 0, TKV_DTYPE_FP16 = 1 };

@@ -98,9 +98,12 @@ __global__ void __launch_bounds__(block_threads(UT), UT > 256 ? 2 : 4) append_ke
         const int t = (int)(w / (uint32_t)a.q_groups), lane = threadIdx.x & 31;
         if (t >= a.T) return;
         int b = t;
-        if (a.cu) {     // the sequence of row t: as many ends as are not behind it
-            b = 0;
-            for (int i = 0; i < c.B; i += 32) b += __popc(__ballot_sync(0xffffffffu, i + lane < c.B && a.cu[i + lane + 1] <= t));
+        if (a.cu) {     // the first sequence that has row t
+            b = c.B;
+            for (int i = 0; i < c.B && b == c.B; i += 32) {
+                const uint32_t has = __ballot_sync(0xffffffffu, i + lane < c.B && a.cu[i + lane] <= t && t < a.cu[i + lane + 1]);
+                if (has) b = i + __ffs(has) - 1;
+            }
         }
         Seq s;
         uint32_t bad = 0;

@@ -378,3 +378,26 @@ def test_a_new_caches_pools_are_ready_for_any_stream(shared):
     torch.cuda.synchronize()
     assert (c.k_pool[3, :, 0].float() * c.k_scale[3][:, None] == 1).all() and (c.v_scale[3] > 0).all()
     del keep
+
+
+# ------------------------------------------------------------------ bad row offsets
+@pytest.mark.parametrize("cu,good", [([0, 4, 2, 2], [0]), ([0, 4, 9, 5, 40, 40], [0, 1]), ([3, 5, -2, -2], [0]),
+                                     ([0, 3, 41, 41], [0]), ([0, 0, 6, 1, 1], [1])])
+def test_queries_of_usable_sequences_beside_row_offsets_that_are_not(cu, good):
+    """Offsets that decrease or leave the rows behind a usable sequence: its rows are encoded and
+    appended, the others' are not, and the fault is latched."""
+    gen = torch.Generator().manual_seed(len(cu))
+    T, B, page, hkv, g, d = 40, len(cu) - 1, 16, 1, 2, 64
+    c = TkvPagedCache(B, hkv, g, d, page, 4 * B, 4)
+    table = torch.arange(4 * B, dtype=torch.int32).view(B, 4)
+    n = [cu[i + 1] - cu[i] if i in good else 0 for i in range(B)]
+    lens = [n[i] + 7 if i in good else 50 for i in range(B)]
+    k, q = torch.randn((T, hkv, d), generator=gen).to(BF16), torch.randn((T, hkv * g, d), generator=gen).to(BF16)
+    out = torch.full_like(q, 9.0).cuda()
+    c.append(k.cuda(), k.cuda(), table.cuda(), _i32(lens).cuda(), cu=_i32(cu).cuda(), max_new=8, q=q.cuda(), q_out=out)
+    assert c.poll_error() == tkv.TKV_ERR_INVALID
+    mine = torch.zeros(T, dtype=torch.bool)
+    for b in good:
+        mine[cu[b]:cu[b + 1]] = True
+        assert (c.k_scale[4 * b] > 0).all()
+    assert torch.equal(out.cpu()[mine], q[mine]) and (out.cpu()[~mine] == 9.0).all()
