@@ -371,9 +371,10 @@ TKV_API int64_t tkv_launch_count(const tkv_cache *cache);
  *   k_pool, v_pool    8-bit [pages][Hkv][page][D]
  *   k_scale, v_scale  fp32  [pages][Hkv]            value = code * scale
  * Codes are signed integers in [-127, 127] (code 0) or FP8 E4M3 (code 1).  Scales are
- * 0 or finite and >= 2^-80; the append writes powers of two from 2^-64 on.  Token j of sequence b is in page
- * block_table[b * max_pages + j / page], slot j % page.  A page that an append writes
- * belongs to one sequence; pages that are only read may be shared.
+ * 0 or finite and >= 2^-80; the append writes powers of two from 2^-64 on.  (The attention's
+ * sums are fp32: a value times the sequence's length is to stay below 2^115.)  Token j of
+ * sequence b is in page block_table[b * max_pages + j / page], slot j % page.  A page that an
+ * append writes belongs to one sequence; pages that are only read may be shared.
  *
  * Lengths, offsets and tables are device memory:
  *   block_table  int32 [B][max_pages]   page of each block of tokens (-1: none)
@@ -485,7 +486,7 @@ typedef struct {
     int32_t max_q;                 /* bound on a sequence's query rows (>= 1); it only
                                       chooses the kernel                          */
     int32_t window;                /* >= 0; from 2^30 on as 0: every key         */
-    float softmax_scale;           /* finite                                     */
+    float softmax_scale;           /* finite, also times log2(e)                 */
 } tkv_paged_attention_args;
 
 /* GQA attention of T query rows over the cache.  Row i of the n rows of sequence b is at

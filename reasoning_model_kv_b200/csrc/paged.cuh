@@ -14,6 +14,7 @@ namespace paged {
 
 constexpr int kMaxGroup = 16;          // query heads per kv head
 constexpr int kMaxLen = 1 << 30;       // tokens of a sequence
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct View {
     int B, Hkv, G, D, page, page_log2, pages, max_pages, code, dtype;

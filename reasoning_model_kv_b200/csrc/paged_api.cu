@@ -189,7 +189,7 @@ tkv_status tkv_paged_attention(tkv_paged *c, const tkv_paged_attention_args *a, 
     if (const char *w = lengths_fault(c, a->block_table, a->kv_len, a->cu, T)) return bad(w);
     if (a->max_q < 1) return bad("max_q must be >= 1");
     if (a->window < 0) return bad("window must be >= 0");
-    if (!std::isfinite(a->softmax_scale)) return bad("softmax_scale must be finite");
+    if (!std::isfinite(a->softmax_scale * tkv::paged::kLog2e)) return bad("softmax_scale must be finite, in units of log2 too");
     if (T == 0) return TKV_OK;
     const Rows q = rows(a->q), out = rows(a->out);
     if (const char *w = rows_fault(q)) return bad(w);

@@ -25,7 +25,7 @@ cudaError_t launch_attention(const View &c, Rows q, Rows out, int T, const int32
     // within 32 bits
     a.window = window >= kMaxLen ? 0 : window;
     a.room = c.max_pages * c.page;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;
     a.arrived = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(c.err) + 256);
     a.cut = reinterpret_cast<CutItem *>(reinterpret_cast<uint8_t *>(a.arrived) + kArrivedBytes);
     a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.cut) + kCutBytes);

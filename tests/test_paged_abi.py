@@ -162,3 +162,10 @@ def test_output_rows_that_overlap_across_tokens_and_heads_are_refused():
         for fn, *a in args:
             assert fn(*a, None) == INV and "overlap" in tkv.lib().tkv_last_error_string().decode(), strides
     assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_destroy(h) == 0
+
+
+def test_softmax_scales_that_leave_fp32_in_log2_units_are_refused():
+    L, h, p = tkv.lib(), _create(), 1 << 24
+    for scale in (3e38, -3e38, 2.4e38):
+        assert L.tkv_paged_attention(h, paged._ATTENTION_ARGS.pack(p, 1024, 128, p, 1024, 128, p, p, 0, 2, 1, 0, scale), None) == INV
+    assert L.tkv_paged_launch_count(h) == 0 and L.tkv_paged_destroy(h) == 0
