@@ -125,10 +125,9 @@ __device__ __forceinline__ void plain_values(uint32_t vt, float f, const float (
     }
 }
 
-template <int D, int NT>
-constexpr int ring_bytes() { return kWarps * kStages * 2 * 16 * D; }
-template <int D, int NT>
-constexpr int smem_bytes() { return ring_bytes<D, NT>(); }
+// the ring; a block's join of four warps' rows takes no more (32 rows of D fp32)
+template <int D>
+constexpr int smem_bytes() { return kWarps * kStages * 2 * 16 * D; }
 
 template <typename T, int D, int CODE, int NT>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
@@ -534,12 +533,12 @@ cudaError_t run(AttnArgs a, cudaStream_t st, int64_t *launches) {
     int sms = 0, per_sm = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e == cudaSuccess) e = cached_blocks_per_sm(occupancy, reinterpret_cast<const void *>(kernel), kThreads,
-                                                   smem_bytes<D, NT>(), &per_sm);
+                                                   smem_bytes<D>(), &per_sm);
     if (e != cudaSuccess) return e;
     a.tile_tokens = 8 * NT / a.c.G;
     a.item_cost = kItemCost;
     const int blocks = min(sms * per_sm, min(kMaxBlocks, kPartRows / (8 * NT)));
-    kernel<<<blocks, kThreads, smem_bytes<D, NT>(), st>>>(a);
+    kernel<<<blocks, kThreads, smem_bytes<D>(), st>>>(a);
     e = cudaGetLastError();
     ++*launches;
     // no item has more units than the block table has room for (key_range)

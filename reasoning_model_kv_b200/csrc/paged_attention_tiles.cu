@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s)
                             tc::mma_f16(tb + kColS + 128 * sub, off(q, (s >> 2) * 16384 + (s & 3) * 32),
-                                        off(kk, (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0, 1);
-                        tc::commit(smem_addr(&bar.s_full[sub]), 1);
+                                        off(kk, (s >> 2) * 16384 + (s & 3) * 32), kIdS, s > 0);
+                        tc::commit(smem_addr(&bar.s_full[sub]));
                     }
                     __syncwarp();
                 };
@@ -509,13 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
                         for (int s = 0; s < kUnit / 16; ++s)
                             tc::mma_f16_ts(tb + kColO + 128 * sub, tb + kColS + 128 * sub + 8 * s, off(vv, s * 2048), kIdO,
-                                           more || s > 0, 1);
-                        tc::commit(smem_addr(&bar.o_full[sub]), 1);
+                                           more || s > 0);
+                        tc::commit(smem_addr(&bar.o_full[sub]));
                     }
                     __syncwarp();
                 };
                 auto release = [&](uint64_t *b) {
-                    if (tc::elect()) tc::commit(smem_addr(b), 1);
+                    if (tc::elect()) tc::commit(smem_addr(b));
                     __syncwarp();
                 };
                 do {
