@@ -193,19 +193,19 @@ class TkvPagedCache:
         _check(lib().tkv_paged_create(ctypes.byref(self.cfg), self.k_pool.data_ptr(), self.v_pool.data_ptr(),
                                       self.k_scale.data_ptr(), self.v_scale.data_ptr(), base + (-base) % 256, nbytes,
                                       ctypes.byref(h)))
-        self._h = h.value
         self._table_shape, self._len_shape, self._cu_shape = (B, max_pages), (B,), (B + 1,)
-        self._append, self._attention = lib().tkv_paged_append, lib().tkv_paged_attention
+        self._append, self._attention, self._destroy = (lib().tkv_paged_append, lib().tkv_paged_attention,
+                                                        lib().tkv_paged_destroy)
+        self._h = h.value
         if share is None:
             self.reset()
         if share is None or made:
             torch.cuda.current_stream(self.device).synchronize()    # ready for any stream
 
     def __del__(self):
-        h = getattr(self, "_h", None)
-        if h is not None and tkv._lib is not None:
-            tkv._lib.tkv_paged_destroy(h)
-            self._h = None
+        h, self._h = getattr(self, "_h", None), None
+        if h is not None:
+            self._destroy(h)
 
     def _lengths(self, block_table, kv_len, cu, T):
         i = self.index

@@ -3,6 +3,8 @@ table has no room for, windows without an end, value scales far apart, values an
 are not finite, other streams than the current one.  Against 64-bit forms, as in
 tests/test_gpu_paged.py."""
 import math
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -10,7 +12,7 @@ import torch
 import synth
 from reasoning_model_kv_b200 import TkvPagedCache, TkvRope, tkv, tkv_qk_norm_rope
 from tests import paged_oracle as po
-from tests.conftest import gpu_available
+from tests.conftest import ROOT, gpu_available
 from tests.gpu_harness import build_pair
 
 pytestmark = [pytest.mark.gpu,
@@ -401,3 +403,11 @@ def test_queries_of_usable_sequences_beside_row_offsets_that_are_not(cu, good):
         mine[cu[b]:cu[b + 1]] = True
         assert (c.k_scale[4 * b] > 0).all()
     assert torch.equal(out.cpu()[mine], q[mine]) and (out.cpu()[~mine] == 9.0).all()
+
+
+def test_a_cache_that_lives_until_the_interpreter_ends():
+    """Its host object is freed without a word, whatever modules are gone by then."""
+    code = ("from reasoning_model_kv_b200 import TkvPagedCache, paged; "
+            "paged.kept = TkvPagedCache(1, 1, 1, 64, 16, 1, 1); print('made')")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "made" and "__del__" not in r.stderr, r.stderr
