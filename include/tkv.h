@@ -413,7 +413,8 @@ typedef struct {
  *             (a, b) -> (a cos th - b sin th, a sin th + b cos th)
  *             a, b = elements i, i + rot/2 (interleaved 0) or 2i, 2i + 1 (interleaved 1);
  *             elements from rot on stay as they are.
- * Both in fp32 with one rounding at the end; the angle's turns are reduced in fp64. */
+ * Both in fp32 with one rounding at the end; the angle's turns are reduced in fp64, its sine and
+ * cosine are the hardware's, off by 2^-20 at most. */
 typedef struct {
     const float *inv_freq;   /* device fp32 [rot/2], NULL when rot is 0        */
     int32_t rot;             /* rotated elements: a multiple of 8 in [0, D]    */

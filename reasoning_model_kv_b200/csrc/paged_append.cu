@@ -5,10 +5,10 @@
 // magnitude, settle the scale, round what the page held before if the scale grew, and write
 // the codes.  So the rows are read once, a scale has one writer and nothing needs an atomic.
 // Units of small pages share a block.  The queries' rows are blocks of the same launch.
-// Measured: eight prompt chunks (21 thousand tokens, 475 MB) in 100 us = 4.7 TB/s, where the
-// queries' part streams and the units wait for memory and their barrier (the two kinds of
-// blocks in turn were no faster); one token of 64 sequences in 7.6 us, a chain of dependent
-// reads (lengths, page, scale and rows).
+// Measured: eight prompt chunks (21 thousand tokens, 475 MB) in 102 us = 4.7 TB/s (int8 codes 112), where
+// the queries' part streams and the units wait for memory and their barrier (the two kinds of
+// blocks in turn were no faster); one token of 64 sequences in 7.5 us (int8 7.7), a chain of
+// dependent reads (lengths, page, scale and rows) by 1152 blocks in two rounds.
 #include <climits>
 
 #include <cuda_fp8.h>
@@ -272,7 +272,9 @@ template <typename T, int D, int CODE, int UT>
 cudaError_t run(AppendArgs a, cudaStream_t st) {
     constexpr int kBlock = block_threads(UT);
     const long long per = kBlock / UT;
-    // Every sequence may have `slots` pages; all together touch at most T / page + 2 B.
+    // Every sequence may have `slots` pages; all together touch at most T / page + 2 B.  256 sequences of 1
+    // to 2000 new tokens and pages of 16 (6 times as many) take 178 us counted, 215 not; eight prompt
+    // chunks (1.6 times) 105.5 and 101.8; short prompts (3 times) 12.0 either way.
     const long long every = (long long)a.c.B * a.slots, touched = (long long)(a.T >> a.c.page_log2) + 2ll * a.c.B;
     a.compact = every > 4 * touched;
     const long long units = 2 * (a.compact ? touched : every) * a.c.Hkv, kv_blocks = (units + per - 1) / per;

@@ -13,11 +13,11 @@
 // P is fp16 times 2^7: rounded to 11 bits, more than either output type keeps, and to multiples
 // of 2^-31 of the row's largest weight.  The second rounding matters where a value is far larger
 // than those that carry the weight, so keys whose scale is over 2^10 times the smallest one's are
-// multiplied in fp32 (kWide; four times the instructions).
+// multiplied in fp32 (kWide): 64 x 32k tokens 673 us, 1154 with half the pages 2^12 above the others.
 // The maximum moves only when a logit passes it by 2^8, so most tiles rescale nothing.
-// Measured: 64 sequences of 32k E4M3 tokens, 4.30 GB, in 665 us = 6.46 TB/s (copy rate 6.55); one
-// sequence of 131k int8 tokens, 269 MB, in 56 us = 4.8 TB/s (the split's ends and the join); 3 to
-// 6 rows of 16 sequences with four heads a kv head (24 rows), 194 MB, in 72 us = 2.7 TB/s: eight
+// Measured: 64 sequences of 32k E4M3 tokens, 4.30 GB, in 673 us = 6.39 TB/s (copy rate 6.55); one
+// sequence of 131k int8 tokens, 269 MB, in 57 us = 4.7 TB/s (the split's ends and the join); 3 to
+// 6 rows of 16 sequences with four heads a kv head (24 rows), 194 MB, in 74 us = 2.6 TB/s: eight
 // warps of 255 registers an SM leave the latency of their instructions uncovered.
 #include <type_traits>
 
@@ -37,7 +37,8 @@ using attn::transpose8x8;
 
 constexpr int kThreads = 128, kWarps = 4, kUnitLog2 = 6, kUnit = 64;
 constexpr int kStages = 4;
-// An item's setup takes about as long as this many units.
+// An item's setup takes about as long as this many units.  With 0 / 2 / 4 / 8: ragged windows 40.8 /
+// 28.5 / 27.8 / 29.1 us, verification 77.7 / 77.3 / 74.3 / 77.4, one of 131k 58.4 / 57.0 / 56.4 / 57.5.
 constexpr int kItemCost = 4;
 constexpr float kWide = 1024.f;
 // Sums of weights times values: 2^15 above them is room for weights of 2^8 times 2^7.

@@ -20,10 +20,12 @@
 // NaN); warps of their own look for them (the softmax's or the codes' warps would take 1 to 5 %
 // longer).
 //
-// Measured: two chunks of 2048 rows x 32 heads on 14k and 16k keys, 961 GFLOP, in 925 us = 1.04
-// PFLOP/s, 63 % of the library's bf16 product.  Tensor cores and exponentials are each busy 46 %
-// of the time: a unit's softmax follows its S and precedes its O, and the second tile of rows
-// covers only part of that.  Slower: two threads a row (16 softmax warps), the maximum and P in
+// Measured: two chunks of 2048 rows x 32 heads on 14k and 16k keys, 961 GFLOP, in 888 us = 1.08
+// PFLOP/s, 65 % of the library's bf16 product (pages of 16 1037 us, int8 908); with 64-dim heads 734 us;
+// four prompts of 4096 without a prefix, 550 GFLOP, 835 us.  Tensor cores and exponentials are each
+// busy 46 % of the time: a unit's softmax follows its S and precedes its O, and the second tile of
+// rows covers only part of that.  Every instantiation spills (64 to 112 bytes of stack; softmax
+// and codes both).  Slower: two threads a row (16 softmax warps), the maximum and P in
 // one pass with a second one where the maximum moved, an issuing warp for each tile of rows (its
 // products take turns with the other's; 312 -> 380 us on 2048 rows x 16 heads x 8k keys).
 #include <climits>
@@ -47,7 +49,10 @@ using attn::mbar_wait;
 using attn::smem_addr;
 
 constexpr int kThreads = 512, kUnitLog2 = kTileUnitLog2, kUnit = 1 << kUnitLog2;
-constexpr int kItemCost = 2;             // an item's setup takes about as long as this many units
+// An item's setup takes about as long as this many units.  With 0 / 1 / 2 / 4: 64 rows on 4 to 8k tokens
+// 131.2 / 128.6 / 124.4 / 125.4 us, 33 rows on 1000 17.0 / 17.3 / 16.7 / 16.5, prompt chunks 891 / 890 /
+// 887 / 887.
+constexpr int kItemCost = 2;
 constexpr int kChunks = kUnit / 16;      // groups of keys that share a page
 constexpr int kConstSets = 4;
 constexpr int kReaders = 3;              // warps that look for what is left to the join kernel's plain rows

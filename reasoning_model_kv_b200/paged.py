@@ -155,7 +155,7 @@ class TkvPagedCache:
     """One layer's paged 8-bit cache: pools of pages with a scale for each (page, kv head),
     the append that fills them and the attention over them.  `pools` gives existing
     (k_pool, v_pool, k_scale, v_scale) tensors, else they are made, zeroed.  `share` is a cache
-    whose workspace (up to 40 MB) this one uses too: the layers of a model, say, whose calls
+    whose workspace (up to 43 MB) this one uses too: the layers of a model, say, whose calls
     follow one another on one stream."""
 
     def __init__(self, B, Hkv, G, D, page, pages, max_pages, code="e4m3", dtype=torch.bfloat16, pools=None,
