@@ -14,6 +14,7 @@ namespace paged {
 
 constexpr int kMaxGroup = 16;          // query heads per kv head
 constexpr int kMaxLen = 1 << 30;       // tokens of a sequence
+constexpr float kLeastScale = 5.421010862427522e-20f;      // 2^-64, the least that the append writes: of zeros
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct View {

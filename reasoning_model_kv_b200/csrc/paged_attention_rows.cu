@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AttnArgs a) {
         };
         fetch(0, id0, ks0, vs0);
         fetch(32, id1, ks1, vs1);
-        // the smallest value scale but zero of the units so far, at first of the first 64
+        // the smallest value scale of the units so far, at first of the first 64; that of zeros does
+        // not count (a page of zeros would make all others wide)
         float low = INFINITY;
         auto lower = [&](float vs) {
-            vs = vs > 0.f ? vs : INFINITY;
+            vs = vs > 0.f && vs != kLeastScale ? vs : INFINITY;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) vs = fminf(vs, __shfl_xor_sync(kFull, vs, s));
             low = fminf(low, vs);

@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                         uint32_t bad;
                         const int id = load_page(c, a.block_table, k.b, p, &bad);
                         const float vs = id >= 0 ? c.v_scale[(size_t)id * c.Hkv + k.h] : 0.f;
-                        least = fminf(least, vs > 0.f ? vs : INFINITY);
+                        least = fminf(least, vs > 0.f && vs != kLeastScale ? vs : INFINITY);
                         most = fmaxf(most, vs);
                     }
 #pragma unroll

@@ -411,3 +411,23 @@ def test_a_cache_that_lives_until_the_interpreter_ends():
             "paged.kept = TkvPagedCache(1, 1, 1, 64, 16, 1, 1); print('made')")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "made" and "__del__" not in r.stderr, r.stderr
+
+
+@pytest.mark.parametrize("nq,g", [(1, 4), (5, 2), (40, 2), (150, 1)])
+@pytest.mark.parametrize("page,zeros", [(16, (32, 80)), (64, (0, 64)), (64, (128, 256))])
+def test_pages_of_zero_values_beside_others(nq, g, page, zeros):
+    """Values that are zeros for whole pages take the append's least scale; they count in the softmax
+    and add nothing."""
+    gen = torch.Generator().manual_seed(nq)
+    hkv, d, L = 2, 128, 300
+    k, v = (torch.randn((L, hkv, d), generator=gen).to(BF16) for _ in range(2))
+    v[slice(*zeros)] = 0
+    mp = -(-L // page)
+    c = TkvPagedCache(1, hkv, g, d, page, mp, mp)
+    table = torch.randperm(mp, generator=gen).to(torch.int32)[None]
+    c.append(k.cuda(), v.cuda(), table.cuda(), _i32([L]).cuda(), cu=_i32([0, L]).cuda(), max_new=L)
+    assert (c.v_scale == 2.0 ** -64).any()
+    q = torch.randn((nq, hkv * g, d), generator=gen).to(BF16)
+    out = c.attention(q.cuda(), table.cuda(), _i32([L]).cuda(), d ** -0.5, cu=_i32([0, nq]).cuda(), max_q=nq)
+    pools = (c.k_pool, c.v_pool, c.k_scale, c.v_scale)
+    check(out, *exact(q, pools, table, [L], [nq], d ** -0.5, 0, page), BF16)
