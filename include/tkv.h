@@ -500,7 +500,7 @@ typedef struct {
  * row's largest and multiples of 2^-32 of it below; a softmax weight is rounded to 11 bits and,
  * up to 32 rows (G * max_q), to a multiple of 2^-31 of the row's largest weight, with more rows
  * of 2^-21.  Value scales that differ by more than 2^10 within what a row sees do not change
- * that (but for pages at 2^-64, as the append leaves those of zeros), but are slower: up to 32 rows 1.7 times the time where half the keys' scales are that
+ * that (scales of 0 and of 2^-64, as the append leaves pages of zeros, aside), but are slower: up to 32 rows 1.7 times the time where half the keys' scales are that
  * much above the others, with more rows about 200 times for such a sequence and head.
  * A NaN among a token's E4M3 values reaches the rows that see the token and no others; with
  * more than 32 rows it is as slow where some of them see it. */
